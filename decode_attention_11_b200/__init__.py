@@ -9,6 +9,8 @@ no fallback: if the shared library is missing or fails to load, every call raise
     cache = tq.Cache.allocate(B, Hkv, T_cap, k_bits=4, v_bits=4, qjl_m=128, device="cuda")
     tq.quantize(params, k, v, cache, t_offset=0)            # k, v: [B, Hkv, T_new, 128]
     out = tq.decode_attn(params, q, cache, seq_len)          # q: [B, Hq, 128]
+
+Paged caches, their page management and rotary positions are in ``paged.py`` (same names here).
 """
 from __future__ import annotations
 
@@ -36,6 +38,13 @@ TQ_F32 = 0
 TQ_BF16 = 1
 TQ_LAYOUT_PLAIN = 0
 TQ_LAYOUT_MIXED = 1
+TQ_ROPE_HALF = 0
+TQ_ROPE_PAIR = 1
+TQ_PAGES_NO_ROOM = 1
+TQ_PAGES_BAD_INDEX = 2
+TQ_PAGES_NOT_EMPTY = 4
+TQ_PAGES_BAD_LENGTH = 8
+TQ_PAGES_SHARED = 16
 
 # Functions declared in include/tq.h (checked by the test-suite against the header).
 EXPORTED = ("tq_status_string", "tq_last_error", "tq_version", "tq_build_codebook",
@@ -44,7 +53,9 @@ EXPORTED = ("tq_status_string", "tq_last_error", "tq_version", "tq_build_codeboo
             "tq_decode_workspace_size", "tq_decode_attn", "tq_decode_attn_static",
             "tq_decode_static_workspace_limit", "tq_sketch_rotation", "tq_build_hadamard_rotation",
             "tq_decode_step", "tq_decode_step_fused", "tq_decode_device_errors",
-            "tq_reset_device_errors", "tq_debug_quantize_stall")
+            "tq_reset_device_errors", "tq_debug_quantize_stall", "tq_rope", "tq_pages_workspace_size",
+            "tq_pages_reserve", "tq_pages_fork", "tq_pages_free", "tq_pages_compact", "tq_pages_copy",
+            "tq_paged_quantize", "tq_paged_read", "tq_paged_decode_workspace_size", "tq_paged_decode_attn")
 
 
 class TqError(RuntimeError):
@@ -71,6 +82,12 @@ class _Params(ctypes.Structure):
                 ("k_centroids_lo", ctypes.c_void_p), ("k_thresholds_lo", ctypes.c_void_p),
                 ("v_centroids_lo", ctypes.c_void_p), ("v_thresholds_lo", ctypes.c_void_p),
                 ("outlier_mask", ctypes.c_uint32 * 4)]
+
+
+class _PageTable(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -140,6 +157,24 @@ def lib() -> ctypes.CDLL:
     L.tq_sketch_rotation.restype = ctypes.c_int
     L.tq_sketch_rotation.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
                                      ctypes.c_void_p]
+    i32, i64, vp, sz = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+    pc, pp, pt = ctypes.POINTER(_Cache), ctypes.POINTER(_Params), ctypes.POINTER(_PageTable)
+    for name, res, args in (
+            ("tq_rope", i32, [vp, i64, i64, i32, vp, i64, i64, i32, i32, i32, vp, i64, i32, ctypes.c_char_p,
+                              ctypes.c_double, i32, i32, vp, vp, vp]),
+            ("tq_pages_workspace_size", sz, [pt, i32]),
+            ("tq_pages_reserve", i32, [pt, vp, vp, i32, vp, i32, vp, sz, vp]),
+            ("tq_pages_fork", i32, [pt, vp, vp, i32, pc, i32, vp, sz, vp]),
+            ("tq_pages_free", i32, [pt, vp, i32, vp]),
+            ("tq_pages_compact", i32, [pt, pc, i32, vp, sz, vp]),
+            ("tq_pages_copy", i32, [pc, i32, vp, vp, i32, vp, vp]),
+            ("tq_paged_quantize", i32, [pp, vp, vp, i32, i64, i64, i32, vp, pc, vp]),
+            ("tq_paged_read", i32, [pp, pc, vp, i32, i32, vp, vp, vp, vp, vp]),
+            ("tq_paged_decode_workspace_size", sz, [i32, i32, pc]),
+            ("tq_paged_decode_attn", i32, [pp, vp, i32, i32, i32, pc, vp, i64, i32, vp, i32, ctypes.c_float, vp, i32,
+                                           vp, vp, sz, vp])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = res, args
     _lib = L
     return L
 
@@ -469,6 +504,9 @@ def decode_attn_static(params: Params, q: torch.Tensor, cache: Cache, seq_len: i
     return out
 
 
+from .paged import (PageTable, paged_decode_attn, paged_decode_workspace_size, paged_quantize, paged_read,  # noqa: E402
+                    pages_compact, pages_copy, pages_fork, pages_free, pages_reserve, rope)
+
 __all__ = [
     "LIB_PATH", "EXPORTED", "TqError", "lib", "status_string", "last_error", "version",
     "build_codebook", "Params", "Cache", "quantize", "quantize_device_errors",
@@ -478,4 +516,8 @@ __all__ = [
     "debug_quantize_stall", "decode_step", "decode_step_fused",
     "TQ_OK", "TQ_ERR_INVALID_ARG", "TQ_ERR_UNSUPPORTED", "TQ_ERR_NO_CONVERGENCE",
     "TQ_ERR_WORKSPACE", "TQ_ERR_CUDA", "TQ_F32", "TQ_BF16", "TQ_LAYOUT_PLAIN", "TQ_LAYOUT_MIXED",
+    "PageTable", "rope", "pages_reserve", "pages_fork", "pages_free", "pages_compact", "pages_copy",
+    "paged_quantize", "paged_read", "paged_decode_attn", "paged_decode_workspace_size",
+    "TQ_ROPE_HALF", "TQ_ROPE_PAIR", "TQ_PAGES_NO_ROOM", "TQ_PAGES_BAD_INDEX", "TQ_PAGES_NOT_EMPTY",
+    "TQ_PAGES_BAD_LENGTH", "TQ_PAGES_SHARED",
 ]

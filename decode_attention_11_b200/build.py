@@ -9,6 +9,7 @@ of touching memory).  The package loads it when ``TQ_DEBUG=1`` is set in the env
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
 import sys
@@ -20,8 +21,12 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtq_b200.so")
 DEBUG_LIB = os.path.join(HERE, "libtq_b200_debug.so")
 DEBUG_SOURCES = ("tq_decode.cu",)  # the sources that hold TQ_DEBUG checks
-SOURCES = ["tq_host.cpp", "tq_quantize.cu", "tq_quantize_pipe.cu", "tq_decode.cu"]
+SOURCES = ["tq_host.cpp", "tq_quantize.cu", "tq_quantize_pipe.cu", "tq_decode.cu", "tq_rope.cu", "tq_pages.cu",
+           "tq_paged_rows.cu", "tq_paged_decode.cu", "tq_paged_split_k2.cu", "tq_paged_split_k3.cu",
+           "tq_paged_split_k4.cu"]
 HEADERS = [os.path.join(CSRC, "tq_internal.h"), os.path.join(CSRC, "tq_sm100.h"),
+           os.path.join(CSRC, "tq_decode_core.h"), os.path.join(CSRC, "tq_paged.h"),
+           os.path.join(CSRC, "tq_paged_split.cuh"),
            os.path.join(INCLUDE, "tq.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
@@ -32,12 +37,12 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale(lib: str) -> bool:
-    if not os.path.exists(lib):
-        return True
-    t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS + [os.path.abspath(__file__)]
-    return any(os.path.getmtime(d) > t for d in deps)
+def _stale(out: str, deps) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(d) > os.path.getmtime(out) for d in deps)
+
+
+def _stale_object(src: str, obj: str) -> bool:
+    return _stale(obj, [os.path.join(CSRC, src), os.path.abspath(__file__)] + HEADERS)
 
 
 def _compile(src: str, obj: str, extra: list, verbose: bool) -> None:
@@ -45,6 +50,13 @@ def _compile(src: str, obj: str, extra: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
+
+
+def _compile_all(jobs: list, verbose: bool) -> None:
+    """Compile (source, object, extra flags) jobs side by side, one per host core."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        for f in [pool.submit(_compile, *j, verbose) for j in jobs]:
+            f.result()
 
 
 def _link(objs: list, lib: str) -> None:
@@ -59,16 +71,17 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = {src: os.path.join(objdir, src.rsplit(".", 1)[0] + ".o") for src in SOURCES}
-    if force or _stale(LIB):
-        for src in SOURCES:
-            _compile(src, objs[src], [], verbose)
+    debug_objs = {src: os.path.join(objdir, src.rsplit(".", 1)[0] + "_debug.o") for src in DEBUG_SOURCES}
+    jobs = [(src, obj, []) for src, obj in objs.items() if force or _stale_object(src, obj)]
+    if debug:
+        jobs += [(src, obj, ["-DTQ_DEBUG"]) for src, obj in debug_objs.items() if force or _stale_object(src, obj)]
+    _compile_all(jobs, verbose)
+    if force or _stale(LIB, objs.values()):
         _link(list(objs.values()), LIB)
     if not debug:
         return LIB
-    if force or _stale(DEBUG_LIB) or os.path.getmtime(LIB) > os.path.getmtime(DEBUG_LIB):
-        for src in DEBUG_SOURCES:
-            objs[src] = os.path.join(objdir, src.rsplit(".", 1)[0] + "_debug.o")
-            _compile(src, objs[src], ["-DTQ_DEBUG"], verbose)
+    objs.update(debug_objs)
+    if force or _stale(DEBUG_LIB, objs.values()):
         _link(list(objs.values()), DEBUG_LIB)
     return DEBUG_LIB
 

@@ -56,6 +56,18 @@ tq_status check_cache(const tq_cache* c) {
   return TQ_OK;
 }
 
+tq_status check_pool(const tq_cache* c) {
+  const tq_status st = check_cache(c);
+  if (st != TQ_OK) return st;
+  if (c->layout != TQ_LAYOUT_PLAIN) return fail(TQ_ERR_UNSUPPORTED, "paged pools have the plain layout");
+  if (c->T_cap % kPageTokens) return fail(TQ_ERR_INVALID_ARG, "page size %d (a multiple of %d)", c->T_cap, kPageTokens);
+  if ((int64_t)c->B * c->T_cap > 0x7fffffff)
+    return fail(TQ_ERR_INVALID_ARG, "pool of %d pages of %d tokens: slots pass 2^31 - 1", c->B, c->T_cap);
+  if ((int64_t)c->Hkv * c->T_cap * 64 > 0x7fffffff)
+    return fail(TQ_ERR_INVALID_ARG, "page of %d kv-heads x %d tokens too large", c->Hkv, c->T_cap);
+  return TQ_OK;
+}
+
 tq_status check_params(const tq_params* p, const tq_cache* c) {
   if (!p) return fail(TQ_ERR_INVALID_ARG, "params is NULL");
   if (!p->Pi || !p->k_centroids || !p->k_thresholds || !p->v_centroids || !p->v_thresholds)

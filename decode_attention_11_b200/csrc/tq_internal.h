@@ -36,6 +36,8 @@ void clear_error();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // Packed-row slot maps (the cache layout documented in tq.h).
 // Key-code rows and sign rows are ordered for the decode kernel's m16n8k16 B fragments:
 // thread tau of a quad owns coordinates 16*a + 8*h + 2*tau + e.
@@ -69,11 +71,25 @@ __host__ __device__ inline int sign_bit_of_row(int l) {
   return 32 * t + (2 * a + h) + 16 * e;
 }
 
+// Row of a paged pool (pages of `ps` tokens, row ((page * Hkv) + h) * ps + place) that slot `slot` has in
+// kv-head h; -1 for a slot outside the pool.
+__host__ __device__ inline int64_t slot_row(int slot, int h, int Hkv, int pages, int ps) {
+  if (slot < 0) return -1;
+  const int page = slot / ps;
+  if (page >= pages) return -1;
+  return ((int64_t)page * Hkv + h) * ps + (slot - page * ps);
+}
+
 // bf16 quantize pipeline (tq_quantize_pipe.cu).  Sets *handled = false, and enqueues nothing,
 // when the inputs cannot be described by a TMA tensor map.
+// With `slots` (T_new device int32) the cache is a paged pool: the inputs are [T_new, Hkv, 128]
+// (sb unused) and token t goes to slot slots[t].
 tq_status quantize_bf16_pipeline(const tq_params* p, const void* k, const void* v, int64_t sb, int64_t sh,
-                                 int64_t st, int T_new, int t_offset, const tq_cache* c, int sms,
+                                 int64_t st, int T_new, int t_offset, const int32_t* slots, const tq_cache* c, int sms,
                                  struct CUstream_st* stream, bool* handled);
+// General quantize kernel (tq_quantize.cu) over tokens of a paged pool, fp32 or bf16.
+tq_status quantize_general_paged(const tq_params* p, const void* k, const void* v, int dtype, int64_t sn, int64_t sh,
+                                 int N, const int32_t* slots, const tq_cache* c, int sms, struct CUstream_st* stream);
 unsigned int pipe_device_errors();
 long long pipe_vector_fixups();
 long long pipe_code_fixups();
@@ -86,5 +102,9 @@ long long pipe_exempt_signs();
 // Validation shared by tq_quantize / tq_decode_attn.
 tq_status check_params(const tq_params* p, const tq_cache* c);
 tq_status check_cache(const tq_cache* c);
+// A cache that is a pool of pages: check_cache, the plain layout, a page size that is a multiple of
+// kPageTokens, and slots that fit int32.
+constexpr int kPageTokens = 16;
+tq_status check_pool(const tq_cache* c);
 
 }  // namespace tq

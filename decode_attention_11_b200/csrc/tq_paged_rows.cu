@@ -1,0 +1,432 @@
+// Rows of a paged pool: tq_paged_quantize (rows into pages) and tq_paged_read (rows back as values).
+//
+// Quantize has two routes.  Many rows go through the tcgen05 pipeline of tq_quantize (or its general
+// kernel for fp32), which take a slot per token.  A decode step's few rows would leave that pipeline
+// with a tile or two per SM and its full depth of latency, so they have a kernel of their own here:
+// a CTA takes up to ROWS (token, kv-head) rows, holds a quarter row of Pi, then of S, per thread in
+// fp64 registers, and does the definition's arithmetic directly in fp64:
+//   n = ||x||, u = sqrt(128) Pi x / n, idx = #{t_i <= u}, rho = u - c[idx], ||r|| = n ||rho|| / sqrt(128),
+//   sign bits of S rho.
+// No guard bands and no second pass are needed.  It is bound by fp64 arithmetic: 49152 products a row.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "tq_internal.h"
+
+namespace tq {
+namespace {
+
+constexpr int D = kHeadDim;
+constexpr unsigned FULL = 0xffffffffu;
+
+struct RowArgs {
+  const void* k;
+  const void* v;
+  int64_t sn, sh;
+  int in_f32;
+  int N, Hkv, rows;  // rows: (token, kv-head) rows of a CTA
+  const int32_t* slots;
+  int pages, ps;
+  int k_bits, v_bits, qjl;
+  uint8_t* k_codes;
+  uint8_t* k_signs;
+  float* k_norm;
+  float* k_rnorm;
+  uint8_t* v_codes;
+  float* v_norm;
+  const float* Pi;
+  const float* S;
+  const float* kc;
+  const float* kt;
+  const float* vc;
+  const float* vt;
+};
+
+constexpr int ROWS = 4;
+// Rows per SM up to which the fp64 kernel is used (about 0.5 us a row and SM, against the pipeline's
+// fixed cost).
+constexpr int kRowKernelPerSm = 32;
+constexpr int QT = 512;  // threads: four per coordinate
+
+struct RowSmem {
+  double x[2 * ROWS][D];   // keys (rows 0 .. ROWS-1), values
+  double rho[ROWS][D];
+  double n[2 * ROWS];
+  double r2[ROWS];
+  uint32_t kw[ROWS][16], vw[ROWS][16], sw[ROWS][4];  // packed rows
+  float kc[16], kt[16], vc[16], vt[16];
+};
+
+// A thread's quarter of row j of a matrix: float4 4 k + q of the row, k = 0 .. 7, in fp64.
+__device__ __forceinline__ void load_quarter(const float* M, int j, int q, double (&m)[32]) {
+  const float4* p = reinterpret_cast<const float4*>(M + j * D) + q;
+  float4 f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = __ldg(p + 4 * k);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    m[4 * k] = (double)f[k].x;
+    m[4 * k + 1] = (double)f[k].y;
+    m[4 * k + 2] = (double)f[k].z;
+    m[4 * k + 3] = (double)f[k].w;
+  }
+}
+// The row's dot product with x (shared memory), on all four threads of the row.
+__device__ __forceinline__ double dot_quarter(const double (&m)[32], const double* x, int q) {
+  double a0 = 0.0, a1 = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const double2* v = reinterpret_cast<const double2*>(x + 16 * k + 4 * q);
+    const double2 v0 = v[0], v1 = v[1];
+    a0 = fma(m[4 * k], v0.x, a0);
+    a1 = fma(m[4 * k + 1], v0.y, a1);
+    a0 = fma(m[4 * k + 2], v1.x, a0);
+    a1 = fma(m[4 * k + 3], v1.y, a1);
+  }
+  double acc = a0 + a1;
+  acc += __shfl_xor_sync(FULL, acc, 1);
+  acc += __shfl_xor_sync(FULL, acc, 2);
+  return acc;
+}
+__device__ __forceinline__ double warp_sumsq(const double* x) {
+  const int lane = threadIdx.x & 31;
+  double acc = 0.0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc = fma(x[lane + 32 * k], x[lane + 32 * k], acc);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(FULL, acc, o);
+  return acc;
+}
+__device__ __forceinline__ void put_code(uint32_t* w, int bit, int bits, uint32_t code) {
+  atomicOr(w + (bit >> 5), code << (bit & 31));
+  if ((bit & 31) + bits > 32) atomicOr(w + (bit >> 5) + 1, code >> (32 - (bit & 31)));
+}
+
+__global__ void __launch_bounds__(QT, 1) quantize_rows(const __grid_constant__ RowArgs a) {
+  __shared__ RowSmem s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int j = tid >> 2, q = tid & 3;
+  const int64_t r0 = (int64_t)blockIdx.x * a.rows;
+  const int nr = (int)min((int64_t)a.rows, (int64_t)a.N * a.Hkv - r0);
+  double m[32];
+  load_quarter(a.Pi, j, q, m);
+  for (int i = tid; i < 2 * nr * D; i += QT) {
+    const int v = i / D, e = i % D, row = v < nr ? v : v - nr;
+    const int64_t n = (r0 + row) / a.Hkv, h = (r0 + row) % a.Hkv;
+    const int64_t at = n * a.sn + h * a.sh + e;
+    const void* src = v < nr ? a.k : a.v;
+    s.x[v < nr ? row : ROWS + row][e] = a.in_f32 ? (double)reinterpret_cast<const float*>(src)[at]
+                                                : (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src)[at]);
+  }
+  if (tid < 16) s.kc[tid] = tid < (1 << a.k_bits) ? a.kc[tid] : 0.0f;
+  else if (tid < 32) s.vc[tid - 16] = tid - 16 < (1 << a.v_bits) ? a.vc[tid - 16] : 0.0f;
+  else if (tid < 48) s.kt[tid - 32] = tid - 32 < (1 << a.k_bits) - 1 ? a.kt[tid - 32] : INFINITY;
+  else if (tid < 64) s.vt[tid - 48] = tid - 48 < (1 << a.v_bits) - 1 ? a.vt[tid - 48] : INFINITY;
+  for (int i = tid; i < ROWS * 36; i += QT) (&s.kw[0][0])[i] = 0u;  // kw, vw and sw lie together
+  static_assert(offsetof(RowSmem, sw) - offsetof(RowSmem, kw) == ROWS * 32 * 4, "packed rows");
+  __syncthreads();
+  if (warp < 2 * ROWS && warp % ROWS < nr) {
+    const double ss = warp_sumsq(s.x[warp]);
+    if (lane == 0) s.n[warp] = sqrt(ss);
+  }
+  __syncthreads();
+  const double sqd = sqrt((double)D);
+  for (int v = 0; v < 2 * nr; ++v) {  // keys, then values
+    const bool isv = v >= nr;
+    const int row = isv ? v - nr : v;
+    const double y = dot_quarter(m, s.x[isv ? ROWS + row : row], q);
+    if (q != (v & 3)) continue;
+    const double n = s.n[isv ? ROWS + row : row];
+    // a zero row, or one with infinities or NaN, has the codes of u = 0
+    const double u = n > 0.0 && n < INFINITY ? sqd * y / n : 0.0;
+    const float* th = isv ? s.vt : s.kt;
+    uint32_t idx = 0;
+#pragma unroll
+    for (int c = 0; c < 15; ++c) idx += u >= (double)th[c] ? 1u : 0u;
+    if (!isv) s.rho[row][j] = u - (double)s.kc[idx];
+    const int bits = isv ? a.v_bits : a.k_bits;
+    put_code(isv ? s.vw[row] : s.kw[row], bits * (isv ? v_slot_of_coord(j) : k_slot_of_coord(j)), bits, idx);
+  }
+  if (a.qjl) load_quarter(a.S, j, q, m);
+  __syncthreads();
+  if (a.qjl) {
+    if (warp < nr) {
+      const double ss = warp_sumsq(s.rho[warp]);
+      if (lane == 0) s.r2[warp] = ss;
+    }
+    for (int row = 0; row < nr; ++row) {
+      const double y = dot_quarter(m, s.rho[row], q);
+      if (q == (row & 3) && y >= 0.0) {
+        const int bit = sign_bit_of_row(j);
+        atomicOr(&s.sw[row][bit >> 5], 1u << (bit & 31));
+      }
+    }
+    __syncthreads();
+  }
+  // one warp writes one row: key words, value words, signs and norms
+  if (warp < nr) {
+    const int64_t n = (r0 + warp) / a.Hkv;
+    const int64_t to = slot_row(a.slots[n], (int)((r0 + warp) % a.Hkv), a.Hkv, a.pages, a.ps);
+    if (to >= 0) {
+      if (lane < 4 * a.k_bits) reinterpret_cast<uint32_t*>(a.k_codes)[to * 4 * a.k_bits + lane] = s.kw[warp][lane];
+      if (lane < 4 * a.v_bits) reinterpret_cast<uint32_t*>(a.v_codes)[to * 4 * a.v_bits + lane] = s.vw[warp][lane];
+      if (a.qjl && lane < 4) reinterpret_cast<uint32_t*>(a.k_signs)[to * 4 + lane] = s.sw[warp][lane];
+      if (lane == 0) {
+        a.k_norm[to] = (float)s.n[warp];
+        a.v_norm[to] = (float)s.n[ROWS + warp];
+        if (a.qjl) a.k_rnorm[to] = (float)(s.n[warp] * sqrt(s.r2[warp]) / sqd);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------- read
+//
+// Eight lanes per row, lane part p holding coordinates 16p .. 16p + 15: in the packed orders those
+// are four runs of four key codes (slots 32t + 4p ..), eight runs of two value codes (slots
+// 16g + 2p ..) and eight bits of each sign word, so a lane needs a few bytes of each array and writes
+// 16 neighbouring values.  Bound by the values written.
+
+struct ReadArgs {
+  int N, Hkv, pages, ps, qjl;
+  const int32_t* slots;
+  const uint8_t* k_codes;
+  const uint8_t* k_signs;
+  const float* k_norm;
+  const float* k_rnorm;
+  const uint8_t* v_codes;
+  const float* v_norm;
+  const float* kc;
+  const float* vc;
+  void* k_out;
+  void* v_out;
+  int8_t* signs;
+  float* rnorm;
+};
+
+// `len` (<= 16) bits at bit `bit` of a row, by bytes (the second only where the bits reach it).
+template <int LEN>
+__device__ __forceinline__ uint32_t bits_at(const uint8_t* row, int bit) {
+  const uint8_t* p = row + (bit >> 3);
+  const int sh = bit & 7;
+  uint32_t w = p[0];
+  if (LEN > 8 || sh + LEN > 8) w |= (uint32_t)p[1] << 8;
+  return (w >> sh) & ((1u << LEN) - 1u);
+}
+
+template <typename T>
+__device__ __forceinline__ void store16(T* dst, const float (&v)[16]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+constexpr int RT = 256;
+
+template <int KB, int VB, typename T>
+__global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs a) {
+  __shared__ float kc[16], vc[16];
+  if (threadIdx.x < 16) kc[threadIdx.x] = threadIdx.x < (1 << KB) ? a.kc[threadIdx.x] : 0.0f;
+  else if (threadIdx.x < 32) vc[threadIdx.x - 16] = threadIdx.x - 16 < (1 << VB) ? a.vc[threadIdx.x - 16] : 0.0f;
+  const int64_t r = ((int64_t)blockIdx.x * RT + threadIdx.x) >> 3;
+  const int p = threadIdx.x & 7;
+  const bool live = r < (int64_t)a.N * a.Hkv;
+  int64_t row = -1;
+  if (live) {
+    const int n = (int)(r / a.Hkv);
+    row = slot_row(a.slots[n], (int)(r - (int64_t)n * a.Hkv), a.Hkv, a.pages, a.ps);
+  }
+  uint32_t kq[4] = {0, 0, 0, 0}, vq[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  uint4 sg = make_uint4(0, 0, 0, 0);
+  float kn = 0.0f, vn = 0.0f, rn = 0.0f;
+  if (row >= 0) {
+    const uint8_t* kr = a.k_codes + row * (16 * KB);
+    const uint8_t* vr = a.v_codes + row * (16 * VB);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (KB == 4) kq[t] = *reinterpret_cast<const uint16_t*>(kr + 16 * t + 2 * p);
+      else kq[t] = bits_at<4 * KB>(kr, KB * (32 * t + 4 * p));
+    }
+#pragma unroll
+    for (int g = 0; g < 8; ++g) vq[g] = bits_at<2 * VB>(vr, VB * (16 * g + 2 * p));
+    kn = a.k_norm[row] * 0.08838834764831845f;  // 1 / sqrt(128)
+    vn = a.v_norm[row] * 0.08838834764831845f;
+    if (a.signs) sg = *reinterpret_cast<const uint4*>(a.k_signs + row * 16);
+    if (a.rnorm) rn = a.k_rnorm[row];
+  }
+  __syncthreads();
+  if (!live) return;
+  float v[16];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int x = 0; x < 4; ++x)  // slot 32t + 4p + x is coordinate 16p + 8 (x / 2) + 2t + x % 2
+      v[8 * (x >> 1) + 2 * t + (x & 1)] = kc[(kq[t] >> (KB * x)) & ((1u << KB) - 1u)] * kn;
+  store16(reinterpret_cast<T*>(a.k_out) + r * D + 16 * p, v);
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+#pragma unroll
+    for (int x = 0; x < 2; ++x)  // slot 16g + 2p + x is coordinate 16p + 8x + g
+      v[8 * x + g] = vc[(vq[g] >> (VB * x)) & ((1u << VB) - 1u)] * vn;
+  store16(reinterpret_cast<T*>(a.v_out) + r * D + 16 * p, v);
+  if (a.signs) {
+    // sketch row 16p + 8h + 2t + e is bit 2p + h + 16e of word t: byte 1 or -1 (0: no row)
+    const uint32_t w[4] = {sg.x, sg.y, sg.z, sg.w};
+    uint32_t o[4] = {0, 0, 0, 0};
+    if (row >= 0) {
+#pragma unroll
+      for (int l = 0; l < 16; ++l) {
+        const int h = l >> 3, t = (l >> 1) & 3, e = l & 1;
+        o[l >> 2] |= ((w[t] >> (2 * p + h + 16 * e)) & 1u ? 0x01u : 0xffu) << (8 * (l & 3));
+      }
+    }
+    reinterpret_cast<uint4*>(a.signs)[r * 8 + p] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (a.rnorm && p == 0) a.rnorm[r] = rn;
+}
+
+template <int KB, int VB, typename T>
+void launch_read(const ReadArgs& a, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.N * a.Hkv;
+  read_rows<KB, VB, T><<<(unsigned)((rows * 8 + RT - 1) / RT), RT, 0, s>>>(a);
+}
+template <int KB, int VB>
+void launch_read_t(const ReadArgs& a, int dtype, cudaStream_t s) {
+  if (dtype == TQ_F32) launch_read<KB, VB, float>(a, s);
+  else launch_read<KB, VB, __nv_bfloat16>(a, s);
+}
+template <int KB>
+void launch_read_k(const ReadArgs& a, int vb, int dtype, cudaStream_t s) {
+  if (vb == 2) launch_read_t<KB, 2>(a, dtype, s);
+  else if (vb == 3) launch_read_t<KB, 3>(a, dtype, s);
+  else launch_read_t<KB, 4>(a, dtype, s);
+}
+
+tq_status check_slots(const int32_t* slots, int N, const tq_cache* pool) {
+  if (N < 0) return fail(TQ_ERR_INVALID_ARG, "N %d", N);
+  if (N > 0 && (!slots || !aligned4(slots))) return fail(TQ_ERR_INVALID_ARG, "slots NULL or misaligned");
+  if ((int64_t)N * pool->Hkv > (1LL << 30)) return fail(TQ_ERR_INVALID_ARG, "%d tokens of %d kv-heads: too many rows", N, pool->Hkv);
+  return TQ_OK;
+}
+
+}  // namespace
+}  // namespace tq
+
+extern "C" tq_status tq_paged_quantize(const tq_params* params, const void* k, const void* v, int dtype,
+                                       int64_t stride_n, int64_t stride_h, int N, const int32_t* slots,
+                                       const tq_cache* pool, void* stream) {
+  using namespace tq;
+  const NvtxRange nvtx_range("tq_paged_quantize");
+  clear_error();
+  tq_status st = check_pool(pool);
+  if (st == TQ_OK) st = check_params(params, pool);
+  if (st == TQ_OK) st = check_slots(slots, N, pool);
+  if (st != TQ_OK) return st;
+  if (dtype != TQ_F32 && dtype != TQ_BF16) return fail(TQ_ERR_UNSUPPORTED, "dtype %d", dtype);
+  if (N == 0) return TQ_OK;
+  const int64_t es = dtype == TQ_F32 ? 4 : 2;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return fail(TQ_ERR_INVALID_ARG, "k / v NULL or not 16-byte aligned");
+  if (stride_n < 0 || stride_h < 0 || (stride_n * es) % 16 || (stride_h * es) % 16)
+    return fail(TQ_ERR_INVALID_ARG, "strides (%lld, %lld) invalid", (long long)stride_n, (long long)stride_h);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t rows = (int64_t)N * pool->Hkv;
+  if (rows > (int64_t)kRowKernelPerSm * sms) {
+    if (dtype == TQ_BF16) {
+      bool handled = false;
+      st = quantize_bf16_pipeline(params, k, v, 0, stride_h, stride_n, N, 0, slots, pool, sms, s, &handled);
+      if (handled || st != TQ_OK) return st;
+    }
+    return quantize_general_paged(params, k, v, dtype, stride_n, stride_h, N, slots, pool, sms, s);
+  }
+  RowArgs a;
+  a.k = k;
+  a.v = v;
+  a.sn = stride_n;
+  a.sh = stride_h;
+  a.in_f32 = dtype == TQ_F32;
+  a.N = N;
+  a.Hkv = pool->Hkv;
+  a.rows = (int)std::min<int64_t>(ROWS, (rows + sms - 1) / sms);
+  a.slots = slots;
+  a.pages = pool->B;
+  a.ps = pool->T_cap;
+  a.k_bits = pool->k_bits;
+  a.v_bits = pool->v_bits;
+  a.qjl = pool->qjl_m ? 1 : 0;
+  a.k_codes = pool->k_codes;
+  a.k_signs = pool->k_signs;
+  a.k_norm = pool->k_norm;
+  a.k_rnorm = pool->k_rnorm;
+  a.v_codes = pool->v_codes;
+  a.v_norm = pool->v_norm;
+  a.Pi = params->Pi;
+  a.S = params->S;
+  a.kc = params->k_centroids;
+  a.kt = params->k_thresholds;
+  a.vc = params->v_centroids;
+  a.vt = params->v_thresholds;
+  quantize_rows<<<(unsigned)((rows + a.rows - 1) / a.rows), QT, 0, s>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "paged quantize launch: %s", cudaGetErrorString(e));
+  return TQ_OK;
+}
+
+extern "C" tq_status tq_paged_read(const tq_params* params, const tq_cache* pool, const int32_t* slots, int N, int dtype,
+                                   void* k_out, void* v_out, int8_t* signs_out, float* rnorm_out, void* stream) {
+  using namespace tq;
+  const NvtxRange nvtx_range("tq_paged_read");
+  clear_error();
+  tq_status st = check_pool(pool);
+  if (st == TQ_OK) st = check_params(params, pool);
+  if (st == TQ_OK) st = check_slots(slots, N, pool);
+  if (st != TQ_OK) return st;
+  if (dtype != TQ_F32 && dtype != TQ_BF16) return fail(TQ_ERR_UNSUPPORTED, "dtype %d", dtype);
+  if ((signs_out || rnorm_out) && !pool->qjl_m) return fail(TQ_ERR_INVALID_ARG, "signs / rnorm of a pool without a sketch");
+  if (N == 0) return TQ_OK;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || !aligned16(signs_out) || !aligned4(rnorm_out))
+    return fail(TQ_ERR_INVALID_ARG, "outputs NULL or misaligned");
+  ReadArgs a;
+  a.N = N;
+  a.Hkv = pool->Hkv;
+  a.pages = pool->B;
+  a.ps = pool->T_cap;
+  a.qjl = pool->qjl_m ? 1 : 0;
+  a.slots = slots;
+  a.k_codes = pool->k_codes;
+  a.k_signs = pool->k_signs;
+  a.k_norm = pool->k_norm;
+  a.k_rnorm = pool->k_rnorm;
+  a.v_codes = pool->v_codes;
+  a.v_norm = pool->v_norm;
+  a.kc = params->k_centroids;
+  a.vc = params->v_centroids;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.signs = signs_out;
+  a.rnorm = rnorm_out;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (pool->k_bits == 2) launch_read_k<2>(a, pool->v_bits, dtype, s);
+  else if (pool->k_bits == 3) launch_read_k<3>(a, pool->v_bits, dtype, s);
+  else launch_read_k<4>(a, pool->v_bits, dtype, s);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "paged read launch: %s", cudaGetErrorString(e));
+  return TQ_OK;
+}

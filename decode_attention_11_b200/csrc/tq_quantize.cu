@@ -67,6 +67,8 @@ struct QArgs {
   int64_t sb, sh, st;
   int T_new, t_offset;
   int B, Hkv, T_cap;
+  const int32_t* slots;  // paged pool: slot of each token (B = 1 of the inputs); else NULL
+  int pages;             // pages of the pool (T_cap: tokens of a page)
   int qjl, in_f32;
   uint8_t* k_codes;
   uint8_t* k_signs;
@@ -889,6 +891,8 @@ __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
 
     // ---- 6. coalesced stores of the tile's rows ----
     {
+      const bool paged = !MX && a.slots != nullptr;
+      auto prow = [&](int i) { return slot_row(a.slots[t0 + i], h, a.Hkv, a.pages, a.T_cap); };
       if constexpr (MX) {  // rows of 56 bytes: 8-byte units (any row is 8-byte aligned)
         const uint2* srk = reinterpret_cast<const uint2*>(s.kst);
         uint2* dsk = reinterpret_cast<uint2*>(a.k_codes + row0 * K_ROW);
@@ -899,27 +903,40 @@ __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
       } else {
         const uint4* srk = reinterpret_cast<const uint4*>(s.kst);
         uint4* dsk = reinterpret_cast<uint4*>(a.k_codes + row0 * K_ROW);
-        for (int i = tid; i < nt * KB; i += THREADS) dsk[i] = srk[i];
+        if (paged) {
+          for (int i = tid; i < nt * KB; i += THREADS)
+            if (prow(i / KB) >= 0) reinterpret_cast<uint4*>(a.k_codes)[prow(i / KB) * KB + i % KB] = srk[i];
+        } else {
+          for (int i = tid; i < nt * KB; i += THREADS) dsk[i] = srk[i];
+        }
         const uint4* srv = reinterpret_cast<const uint4*>(s.vst);
         uint4* dsv = reinterpret_cast<uint4*>(a.v_codes + row0 * V_ROW);
-        for (int i = tid; i < nt * VB; i += THREADS) dsv[i] = srv[i];
+        if (paged) {
+          for (int i = tid; i < nt * VB; i += THREADS)
+            if (prow(i / VB) >= 0) reinterpret_cast<uint4*>(a.v_codes)[prow(i / VB) * VB + i % VB] = srv[i];
+        } else {
+          for (int i = tid; i < nt * VB; i += THREADS) dsv[i] = srv[i];
+        }
       }
       const uint4* src;
-      uint4* dst;
       if (a.qjl) {
         src = reinterpret_cast<const uint4*>(s.sst);
-        dst = reinterpret_cast<uint4*>(a.k_signs + row0 * 16);
-        for (int i = tid; i < nt; i += THREADS) dst[i] = src[i];
+        for (int i = tid; i < nt; i += THREADS) {
+          const int64_t to = paged ? prow(i) : row0 + i;
+          if (to >= 0) reinterpret_cast<uint4*>(a.k_signs)[to] = src[i];
+        }
       }
       for (int i = tid; i < nt; i += THREADS) {
+        const int64_t to = paged ? prow(i) : row0 + i;
+        if (to < 0) continue;
         if constexpr (MX) {
-          reinterpret_cast<float2*>(a.k_norm)[row0 + i] = make_float2(s.kn[i], s.kn2[i]);
-          reinterpret_cast<float2*>(a.v_norm)[row0 + i] = make_float2(s.vn[i], s.vn2[i]);
+          reinterpret_cast<float2*>(a.k_norm)[to] = make_float2(s.kn[i], s.kn2[i]);
+          reinterpret_cast<float2*>(a.v_norm)[to] = make_float2(s.vn[i], s.vn2[i]);
         } else {
-          a.k_norm[row0 + i] = s.kn[i];
-          a.v_norm[row0 + i] = s.vn[i];
+          a.k_norm[to] = s.kn[i];
+          a.v_norm[to] = s.vn[i];
         }
-        if (a.qjl) a.k_rnorm[row0 + i] = s.rn[i];
+        if (a.qjl) a.k_rnorm[to] = s.rn[i];
       }
     }
     __syncthreads();
@@ -943,6 +960,34 @@ tq_status launch3(const QArgs& a, int sms, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "quantize launch: %s", cudaGetErrorString(e));
   return TQ_OK;
+}
+
+// What the arguments of a launch take from the layer's constants and the cache.
+void fill_args(QArgs& a, const tq_params* params, const tq_cache* cache, int dtype) {
+  a.B = cache->B;
+  a.Hkv = cache->Hkv;
+  a.T_cap = cache->T_cap;
+  a.slots = nullptr;
+  a.pages = 0;
+  a.qjl = cache->qjl_m ? 1 : 0;
+  a.in_f32 = dtype == TQ_F32;
+  a.k_codes = cache->k_codes;
+  a.k_signs = cache->k_signs;
+  a.k_norm = cache->k_norm;
+  a.k_rnorm = cache->k_rnorm;
+  a.v_codes = cache->v_codes;
+  a.v_norm = cache->v_norm;
+  a.Pi = params->Pi;
+  a.S = params->S;
+  a.kc = params->k_centroids;
+  a.kt = params->k_thresholds;
+  a.vc = params->v_centroids;
+  a.vt = params->v_thresholds;
+  // Fast-path error, measured on B200 over 1.5e7 coordinates with every guard off: a code differed
+  // from the float64 one only within 6.3e-7 of a threshold, a sign only for |S rho| <= 7.8e-6
+  // (exact fp16 operands: bf16 input, or fp32 keys as fp16 hi + lo; Pi as fp16 hi + lo).  The
+  // bands below are >= 4x those.  fp32 values enter as fp16(x) alone (relative 2^-12, ~2e-4 in u).
+  a.guard = dtype == TQ_F32 ? Guards{4e-6f, 4e-3f, 3e-5f} : Guards{4e-6f, 4e-6f, 3e-5f};
 }
 
 template <typename InT>
@@ -977,6 +1022,26 @@ __global__ void __launch_bounds__(kHeadDim) sketch_rotation_kernel(const float* 
 }
 
 }  // namespace
+}  // namespace tq
+
+namespace tq {
+tq_status quantize_general_paged(const tq_params* p, const void* k, const void* v, int dtype, int64_t sn, int64_t sh,
+                                 int N, const int32_t* slots, const tq_cache* c, int sms, cudaStream_t stream) {
+  QArgs a;
+  a.k = k;
+  a.v = v;
+  a.sb = 0;
+  a.sh = sh;
+  a.st = sn;
+  a.T_new = N;
+  a.t_offset = 0;
+  fill_args(a, p, c, dtype);
+  a.B = 1;  // of the inputs
+  a.slots = slots;
+  a.pages = c->B;
+  return dtype == TQ_F32 ? launch<float>(c->k_bits, c->v_bits, a, sms, stream)
+                         : launch<__nv_bfloat16>(c->k_bits, c->v_bits, a, sms, stream);
+}
 }  // namespace tq
 
 extern "C" tq_status tq_sketch_rotation(const float* Pi, const float* S, int qjl_m, double* S_Pi,
@@ -1027,28 +1092,7 @@ extern "C" tq_status tq_quantize(const tq_params* params, const void* k, const v
   a.st = stride_t;
   a.T_new = T_new;
   a.t_offset = t_offset;
-  a.B = cache->B;
-  a.Hkv = cache->Hkv;
-  a.T_cap = cache->T_cap;
-  a.qjl = cache->qjl_m ? 1 : 0;
-  a.in_f32 = dtype == TQ_F32;
-  a.k_codes = cache->k_codes;
-  a.k_signs = cache->k_signs;
-  a.k_norm = cache->k_norm;
-  a.k_rnorm = cache->k_rnorm;
-  a.v_codes = cache->v_codes;
-  a.v_norm = cache->v_norm;
-  a.Pi = params->Pi;
-  a.S = params->S;
-  a.kc = params->k_centroids;
-  a.kt = params->k_thresholds;
-  a.vc = params->v_centroids;
-  a.vt = params->v_thresholds;
-  // Fast-path error, measured on B200 over 1.5e7 coordinates with every guard off: a code differed
-  // from the float64 one only within 6.3e-7 of a threshold, a sign only for |S rho| <= 7.8e-6
-  // (exact fp16 operands: bf16 input, or fp32 keys as fp16 hi + lo; Pi as fp16 hi + lo).  The
-  // bands below are >= 4x those.  fp32 values enter as fp16(x) alone (relative 2^-12, ~2e-4 in u).
-  a.guard = dtype == TQ_F32 ? Guards{4e-6f, 4e-3f, 3e-5f} : Guards{4e-6f, 4e-6f, 3e-5f};
+  fill_args(a, params, cache, dtype);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->layout == TQ_LAYOUT_MIXED) {  // 4-bit outlier half, 3-bit other half (checked above)
     a.kc2 = params->k_centroids_lo;
@@ -1060,7 +1104,7 @@ extern "C" tq_status tq_quantize(const tq_params* params, const void* k, const v
   }
   if (dtype == TQ_BF16) {
     bool handled = false;
-    st = quantize_bf16_pipeline(params, k, v, stride_b, stride_h, stride_t, T_new, t_offset, cache, sms, s,
+    st = quantize_bf16_pipeline(params, k, v, stride_b, stride_h, stride_t, T_new, t_offset, nullptr, cache, sms, s,
                                 &handled);
     if (handled || st != TQ_OK) return st;
   }

@@ -107,6 +107,8 @@ struct PArgs {
   int64_t sb, sh, st;
   int T_new, t_offset;
   int B, Hkv, T_cap;
+  const int32_t* slots;  // paged pool: slot of each token (B = 1 of the inputs); else NULL
+  int pages;             // pages of the pool (T_cap: tokens of a page)
   int qjl;
   int tiles_per_bh;
   int64_t total_tiles;
@@ -171,6 +173,12 @@ struct __align__(1024) PSmem {
 };
 
 static_assert(sizeof(PSmem) <= 232448, "shared memory per CTA");
+
+// Cache row of token t of (b, h); -1: a paged token that has no place (padding).
+__device__ __forceinline__ int64_t cache_row(const PArgs& a, int b, int h, int t) {
+  if (a.slots) return slot_row(a.slots[t], h, a.Hkv, a.pages, a.T_cap);
+  return ((int64_t)b * a.Hkv + h) * a.T_cap + a.t_offset + t;
+}
 
 // Byte offset of 16-byte chunk c (0..15) of row r of a [128 x 128] 16-bit operand tile: two
 // 64-element K atoms of 16 KB, 8-row groups 1024 bytes apart, chunks XOR-swizzled by (r % 8)
@@ -600,7 +608,8 @@ __device__ __forceinline__ void fix_entry(PSmem& s, const PArgs& a, const FixEnt
   const int t = (int)(E.tile % (uint32_t)a.tiles_per_bh) * TM + E.r;
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   const int64_t in_off = (int64_t)b * a.sb + (int64_t)h * a.sh + (int64_t)t * a.st;
-  const int64_t row = ((int64_t)b * a.Hkv + h) * a.T_cap + a.t_offset + t;
+  const int64_t row = cache_row(a, b, h, t);
+  if (row < 0) return;
   const double sqd = sqrt((double)D);
   unsigned int ncodes = 0, nexempt = 0;
   if (E.flags & 2) {
@@ -918,6 +927,21 @@ __device__ __forceinline__ void copy_rows(const uint8_t* st, int pitch, uint8_t*
   }
 }
 
+// Rows of a warp (lane l: row base + l of the staged array, cache row `row`, -1: none) to the places
+// of a paged pool, 16 bytes per lane, C lanes per row.
+template <int C>
+__device__ __forceinline__ void scatter_rows(const uint8_t* st, int pitch, uint8_t* g, int base, int64_t row) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int c0 = 0; c0 < 32 * C; c0 += 32) {
+    const int i = (c0 + lane) / C, q = (c0 + lane) % C;
+    const int64_t to = __shfl_sync(0xffffffffu, row, i);
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(st + (base + i) * pitch + 16 * q);
+    if (to >= 0) reinterpret_cast<uint4*>(g)[to * C + q] = make_uint4(src[0], src[1], src[2], src[3]);
+  }
+}
+
 // ================================================================ conversion + signs + stores (warps 0-3)
 // Iteration it converts tile it (one row per thread, in place to fp16; norms and row info), then
 // finishes tile it-1: sign bits of S rho (thread = TMEM lane = row, all 128 sketch rows), and,
@@ -1011,7 +1035,8 @@ __device__ __noinline__ void role_conv(const PArgs& a, uint32_t tmem, int n_tile
     // ---- the epilogue has staged the codes of tile ut: copy the tile out ----
     if (!pwait_w(s, &s.fw, ut & 1)) break;
     if (ut == 0) wait_prior_grid();
-    if (r < nt && (smk[0] | smk[1] | smk[2] | smk[3])) {
+    const int64_t prow = a.slots && r < nt ? cache_row(a, b, h, t0 + r) : -1;
+    if (r < nt && (smk[0] | smk[1] | smk[2] | smk[3]) && (!a.slots || prow >= 0)) {
       FixEntry E;
       E.tile = (uint32_t)tile;
       E.r = (uint16_t)r;
@@ -1024,14 +1049,21 @@ __device__ __noinline__ void role_conv(const PArgs& a, uint32_t tmem, int n_tile
       E.seqt = (uint32_t)ut;
       push_fix(s, a, E);
     }
-    copy_rows<KB>(s.kst, 16 * KB + 4, a.k_codes + row0 * (16 * KB), nt, tid);
-    copy_rows<VB>(s.vst, 16 * VB + 4, a.v_codes + row0 * (16 * VB), nt, tid);
-    if (qjl) copy_rows<1>(s.sst, 16, a.k_signs + row0 * 16, nt, tid);
-    if (r < nt) {
+    if (a.slots) {
+      scatter_rows<KB>(s.kst, 16 * KB + 4, a.k_codes, 32 * warp, prow);
+      scatter_rows<VB>(s.vst, 16 * VB + 4, a.v_codes, 32 * warp, prow);
+      if (qjl) scatter_rows<1>(s.sst, 16, a.k_signs, 32 * warp, prow);
+    } else {
+      copy_rows<KB>(s.kst, 16 * KB + 4, a.k_codes + row0 * (16 * KB), nt, tid);
+      copy_rows<VB>(s.vst, 16 * VB + 4, a.v_codes + row0 * (16 * VB), nt, tid);
+      if (qjl) copy_rows<1>(s.sst, 16, a.k_signs + row0 * 16, nt, tid);
+    }
+    const int64_t rown = a.slots ? prow : row0 + r;
+    if (r < nt && rown >= 0) {
       const float nk = s.nrk[bb][r];
-      a.k_norm[row0 + r] = nk;
-      a.v_norm[row0 + r] = s.nrv[bb][r];
-      if (qjl) a.k_rnorm[row0 + r] = nk * sqrtf(s.rho2[0][r] + s.rho2[1][r]) * (1.0f / 11.313708498984761f);
+      a.k_norm[rown] = nk;
+      a.v_norm[rown] = s.nrv[bb][r];
+      if (qjl) a.k_rnorm[rown] = nk * sqrtf(s.rho2[0][r] + s.rho2[1][r]) * (1.0f / 11.313708498984761f);
     }
     __threadfence_block();
     __syncwarp();
@@ -1258,7 +1290,7 @@ __device__ __noinline__ void coop_slow_rows(const PArgs& a) {
     const int t = (int)(tile % (uint32_t)a.tiles_per_bh) * TM + r;
     const int b = bh / a.Hkv, h = bh % a.Hkv;
     const int64_t in_off = (int64_t)b * a.sb + (int64_t)h * a.sh + (int64_t)t * a.st;
-    const int64_t row = ((int64_t)b * a.Hkv + h) * a.T_cap + a.t_offset + t;
+    const int64_t row = cache_row(a, b, h, t);  // (a row without a place was never queued)
     // 1. the input row in fp64 and ||x||^2 (warps 0 and 1)
     if (tid < 64) {
       const uint32_t w2 = reinterpret_cast<const uint32_t*>(a.k + in_off)[tid];
@@ -1513,11 +1545,12 @@ tq_status launch_kv(const PArgs& a, const CUtensorMap& mk, const CUtensorMap& mv
 // bf16 pipeline; returns TQ_OK with *handled = false when the inputs cannot be described by a
 // TMA tensor map (the caller then uses the general kernel).
 tq_status quantize_bf16_pipeline(const tq_params* p, const void* k, const void* v, int64_t sb, int64_t sh,
-                                 int64_t st, int T_new, int t_offset, const tq_cache* c, int sms,
+                                 int64_t st, int T_new, int t_offset, const int32_t* slots, const tq_cache* c, int sms,
                                  cudaStream_t stream, bool* handled) {
   *handled = false;
+  const int B = slots ? 1 : c->B;  // batch of the inputs
   CUtensorMap mk, mv;
-  if (!make_map(&mk, k, c->B, c->Hkv, T_new, sb, sh, st) || !make_map(&mv, v, c->B, c->Hkv, T_new, sb, sh, st))
+  if (!make_map(&mk, k, B, c->Hkv, T_new, sb, sh, st) || !make_map(&mv, v, B, c->Hkv, T_new, sb, sh, st))
     return TQ_OK;
   PArgs a;
   a.k = reinterpret_cast<const __nv_bfloat16*>(k);
@@ -1527,12 +1560,14 @@ tq_status quantize_bf16_pipeline(const tq_params* p, const void* k, const void* 
   a.st = st;
   a.T_new = T_new;
   a.t_offset = t_offset;
-  a.B = c->B;
+  a.B = B;
   a.Hkv = c->Hkv;
   a.T_cap = c->T_cap;
+  a.slots = slots;
+  a.pages = c->B;
   a.qjl = c->qjl_m ? 1 : 0;
   a.tiles_per_bh = (T_new + TM - 1) / TM;
-  a.total_tiles = (int64_t)c->B * c->Hkv * a.tiles_per_bh;
+  a.total_tiles = (int64_t)B * c->Hkv * a.tiles_per_bh;
   if (a.total_tiles >= (1LL << 32)) return TQ_OK;
   a.k_codes = c->k_codes;
   a.k_signs = c->k_signs;

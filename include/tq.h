@@ -276,7 +276,8 @@ tq_status tq_decode_attn(const tq_params* params, const void* q, int q_dtype, in
  * here and the call's output is not valid.
  *   bit 0: a pipeline wait timed out;  bit 1: the device's shared memory per block was too small
  *   for the pipeline;  bits 2 and 3 (only in the library built with -DTQ_DEBUG): a pipeline stage's
- *   cache rows or shared-memory slot, or a partial's slot, failed its bounds check and was skipped.
+ *   cache rows or shared-memory slot, or a partial's slot, failed its bounds check and was skipped;  bit 4: tq_paged_decode_attn met a
+ *   page number or a length out of range.
  *   0 = no error since the library was loaded; -1 if the device could not be queried.
  */
 int tq_decode_device_errors(void);
@@ -344,6 +345,173 @@ tq_status tq_decode_attn_static(const tq_params* params, const void* q, int q_dt
  * be called again in the same process. */
 /* Size in bytes of the static scratch array used by tq_decode_attn_static. */
 size_t tq_decode_static_workspace_limit(void);
+
+/*
+ * Rotary positions of queries and keys, with one or several position axes (text: one; pictures:
+ * height and width; film: time, height and width).  Pair i of a head's 128 coordinates turns by
+ * the angle t = pos[axis_of_pair[i]][n] * base^(-2i/128):
+ *     (a, b) -> (a cos t - b sin t, a sin t + b cos t).
+ * It comes before tq_quantize (keys) and tq_decode_attn (queries); the cache holds rotated keys.
+ *   q, k         device [N, Hq, 128] and [N, Hkv, 128] of dtype (TQ_F32 or TQ_BF16): element (n, h, j)
+ *                at n * stride_n + h * stride_h + j (elements).  Hq or Hkv may be 0 (that pointer is
+ *                then ignored)
+ *   q_out, k_out same shapes, contiguous; may equal q / k when those are contiguous, and must not
+ *                overlap them otherwise
+ *   pos          device int32 [axes][N], row a at pos + a * pos_stride; any int32 value
+ *   axis_of_pair host uint8[64], each < axes
+ *   style        TQ_ROPE_HALF: pair i is coordinates (i, i + 64); TQ_ROPE_PAIR: (2i, 2i + 1)
+ *   inverse      0, or 1 to turn by -t: the inverse, and also the gradient (the rotation is
+ *                orthogonal, so the gradient of x is the inverse applied to the gradient of y)
+ * Angles are reduced modulo one turn in fp64, so far positions keep fp32 accuracy.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (dtype, style), TQ_ERR_CUDA.
+ */
+enum { TQ_ROPE_HALF = 0, TQ_ROPE_PAIR = 1 };
+
+tq_status tq_rope(const void* q, int64_t q_stride_n, int64_t q_stride_h, int Hq, const void* k,
+                  int64_t k_stride_n, int64_t k_stride_h, int Hkv, int dtype, int N, const int32_t* pos,
+                  int64_t pos_stride, int axes, const uint8_t* axis_of_pair, double base, int style,
+                  int inverse, void* q_out, void* k_out, void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Paged caches.
+ *
+ * A pool is a tq_cache of TQ_LAYOUT_PLAIN whose B is the number of pages and whose T_cap is the page
+ * size in tokens (a multiple of 16): page p of kv-head h holds rows ((p * Hkv) + h) * page_size ...
+ * A slot is the number page * page_size + row of one token's place in every kv-head of a pool.
+ *
+ * Which sequence owns which pages is kept in four int32 arrays on the device, changed only by the
+ * calls below, so a serving loop needs no synchronisation and can be captured in a CUDA graph:
+ *   table     [n_seq, max_pages]  pool page of each page of a sequence, -1 where it has none
+ *   seq_lens  [n_seq]             tokens of each sequence (0: the place is free)
+ *   refs      [num_pages]         how many sequences hold the page (0: the page is free)
+ *   status    [1]                 sticky error bits (below); clear it with a memset
+ * Free pages are handed out lowest number first, in the order of the request, so results are
+ * reproducible.  Calls on one page table must be ordered on one stream.  Lists of sequences and
+ * pages are device arrays, whose values only the device can check: a call that finds a bad value
+ * records it in `status`.  tq_pages_reserve and tq_pages_fork then change nothing else.
+ */
+typedef struct {
+  int n_seq, max_pages, num_pages, page_size;
+  int32_t* table;
+  int32_t* seq_lens;
+  int32_t* refs;
+  int32_t* status;
+} tq_page_table;
+
+enum {
+  TQ_PAGES_NO_ROOM = 1,    /* fewer free pages than the call needs */
+  TQ_PAGES_BAD_INDEX = 2,  /* a sequence or page number out of range, or listed twice */
+  TQ_PAGES_NOT_EMPTY = 4,  /* fork into a sequence that has tokens, or that is also a source */
+  TQ_PAGES_BAD_LENGTH = 8, /* a negative or too large length, or more slots than the caller has room for */
+  TQ_PAGES_SHARED = 16     /* growth inside a page that another sequence holds too */
+};
+
+/* Device workspace of tq_pages_reserve, _fork and _compact for a list of n sequences (compact: any
+ * n).  0 on invalid sizes.  Calls that may overlap need separate workspaces. */
+size_t tq_pages_workspace_size(const tq_page_table* pt, int n);
+
+/*
+ * Grow sequences: seqs[i] gets new_tokens[i] >= 0 more tokens, with pages for them.
+ *   seqs, new_tokens  device int32 [n], the sequences distinct
+ *   slots             device int32 [n_slots] out (NULL when n_slots = 0): the slots of the new tokens,
+ *                     sequence after sequence in the order of the list, then -1 up to n_slots
+ * On an error (NO_ROOM, BAD_INDEX, BAD_LENGTH, SHARED) every slot is -1 and nothing else changes.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_WORKSPACE, TQ_ERR_CUDA.
+ */
+tq_status tq_pages_reserve(const tq_page_table* pt, const int32_t* seqs, const int32_t* new_tokens, int n,
+                           int32_t* slots, int n_slots, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Fork sequences: the empty dst[i] becomes a copy of src[i].  Full pages are shared; a partly
+ * filled last page is copied, in every pool of `caches`, to a page of its own, so that both can grow.
+ *   src, dst  device int32 [n]; the dst distinct, empty, and in no src place
+ *   caches    n_caches pools (all layers of the model) of equal sizes, B = num_pages, T_cap = page_size
+ * On an error (NO_ROOM, BAD_INDEX, NOT_EMPTY, BAD_LENGTH) nothing changes.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA.
+ */
+tq_status tq_pages_fork(const tq_page_table* pt, const int32_t* src, const int32_t* dst, int n,
+                        const tq_cache* caches, int n_caches, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * Free sequences: their pages lose one holder each, their table rows become -1 and their lengths 0.
+ * A sequence that is empty, or listed before, is left as it is; a number out of range records
+ * BAD_INDEX and is passed over.  Errors: TQ_ERR_INVALID_ARG, TQ_ERR_CUDA.
+ */
+tq_status tq_pages_free(const tq_page_table* pt, const int32_t* seqs, int n, void* stream);
+
+/*
+ * Move the L pages in use to the page numbers 0 .. L-1, in every pool of `caches`, and renumber table
+ * and refs: the j-th page in use with a number >= L goes to the j-th free number below L; the others
+ * stay.  Errors: as tq_pages_fork.
+ */
+tq_status tq_pages_compact(const tq_page_table* pt, const tq_cache* caches, int n_caches, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * Copy page src[i] to page dst[i], i < n, in every pool of `caches` (table and refs are not
+ * touched).  No page may be a destination twice, or destination and source of two pairs (the pairs
+ * are copied in no order); src[i] = dst[i] is allowed.  A pair with a number out of range is passed
+ * over, and records BAD_INDEX in status[0] when `status` is not NULL.
+ *   src, dst  device int32 [n]
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA.
+ */
+tq_status tq_pages_copy(const tq_cache* caches, int n_caches, const int32_t* src, const int32_t* dst, int n,
+                        int32_t* status, void* stream);
+
+/*
+ * Compress N tokens into the pages of a pool: token n's keys and values go to slot slots[n] of every
+ * kv-head, as tq_quantize would write them (same formulas, same exactness).
+ *   k, v   device [N, Hkv, 128] of dtype (TQ_F32 or TQ_BF16); element (n, h, j) at n * stride_n +
+ *          h * stride_h + j (elements, shared by k and v); stride_n and stride_h times the element size
+ *          multiples of 16 bytes
+ *   slots  device int32 [N]; a token whose slot is outside [0, num_pages * page_size) is not written
+ *          (-1: padding).  Slots must be distinct: a row given twice holds parts of both.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (TQ_LAYOUT_MIXED among them), TQ_ERR_CUDA.
+ */
+tq_status tq_paged_quantize(const tq_params* params, const void* k, const void* v, int dtype, int64_t stride_n,
+                            int64_t stride_h, int N, const int32_t* slots, const tq_cache* pool, void* stream);
+
+/*
+ * Read rows of a pool back as values, in the rotated basis (x ~= Pi^T xhat; scores against Pi q need
+ * no rotation back):
+ *   k_out, v_out  device [N, Hkv, 128] contiguous, of dtype: ||x|| / sqrt(128) * c[idx], rounded once
+ *   signs_out     device int8 [N, Hkv, 128]: +1 / -1 per sketch row, NULL to leave out
+ *   rnorm_out     device float [N, Hkv]: ||r||, NULL to leave out
+ *   slots         device int32 [N]; a slot outside the pool reads as zeros; repeats are allowed
+ * signs_out and rnorm_out must be NULL for a pool with qjl_m = 0.
+ * Errors: as tq_paged_quantize.
+ */
+tq_status tq_paged_read(const tq_params* params, const tq_cache* pool, const int32_t* slots, int N, int dtype,
+                        void* k_out, void* v_out, int8_t* signs_out, float* rnorm_out, void* stream);
+
+/* Bytes of device workspace tq_paged_decode_attn needs on the current device, whatever the lengths.
+ * 0 on invalid sizes. */
+size_t tq_paged_decode_workspace_size(int B, int Hq, const tq_cache* pool);
+
+/*
+ * Single-token attention of a batch of sequences over a paged pool (the scores and sums of
+ * tq_decode_attn).  Lengths and pages are read on the device, so one captured graph serves every step.
+ *   q           device [B, Hq, 128] of q_dtype (TQ_F32 or TQ_BF16), contiguous
+ *   pool        qjl_m 0 or 128, TQ_LAYOUT_PLAIN; Hq % pool->Hkv == 0
+ *   table       device int32, row b at table + b * table_stride, max_pages entries each
+ *   seq_lens    device int32 [B]; 0 gives out = 0 and lse = -inf
+ *   window      0, or the number of last tokens that are seen (the others' pages are not read)
+ *   scale       softmax scale; <= 0 selects 1/sqrt(128)
+ *   out         device [B, Hq, 128] of out_dtype (TQ_F32 or TQ_BF16)
+ *   lse         device float [B, Hq] or NULL: log of the sum of exp(scale * est) over the tokens seen
+ *               (joins this result with attention over other tokens)
+ *   workspace   at least tq_paged_decode_workspace_size() bytes, contents ignored; calls that may
+ *               overlap need separate ones
+ * A page number outside the pool (in a page that a length reaches) or a length outside
+ * [0, max_pages * page_size] records bit 4 in tq_decode_device_errors; that sequence's output is then
+ * not valid, the others are.  Rows past a sequence's length are never used, whatever they hold.
+ * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA.
+ */
+tq_status tq_paged_decode_attn(const tq_params* params, const void* q, int q_dtype, int B, int Hq,
+                               const tq_cache* pool, const int32_t* table, int64_t table_stride, int max_pages,
+                               const int32_t* seq_lens, int window, float scale, void* out, int out_dtype,
+                               float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
