@@ -90,6 +90,8 @@ class _PageTable(ctypes.Structure):
                 ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
+_Mask = ctypes.c_uint32 * 4
+_NO_MASK = _Mask()
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -290,7 +292,7 @@ class Params:
                        _ptr(self.k_thresholds), _ptr(self.v_centroids), _ptr(self.v_thresholds),
                        _ptr(self.S_Pi), _ptr(self.k_centroids_lo), _ptr(self.k_thresholds_lo),
                        _ptr(self.v_centroids_lo), _ptr(self.v_thresholds_lo),
-                       (ctypes.c_uint32 * 4)(*self.outlier_mask))
+                       _Mask(*self.outlier_mask) if any(self.outlier_mask) else _NO_MASK)
 
 
 @dataclasses.dataclass

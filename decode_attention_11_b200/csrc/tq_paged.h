@@ -11,7 +11,16 @@
 namespace tq {
 
 constexpr int kGroup = kPageTokens;  // tokens of a group: the unit of work, inside one page
-constexpr int kMinGroups = 11;       // groups a CTA gets at least: one per consumer warp
+
+// Warps of a split CTA: 16 (128 registers a thread) for up to four heads per unit (nb = 1), 12 (168) for
+// up to eight.
+#ifndef PNW1
+#define PNW1 16
+#endif
+#ifndef PNW2
+#define PNW2 12
+#endif
+constexpr int paged_warps(int nb) { return nb == 1 ? PNW1 : PNW2; }
 
 // Groups of 16 tokens that hold the tokens [first, len) a sequence of length n shows; a length outside
 // [0, max_tokens] counts as 0.
@@ -21,24 +30,43 @@ __host__ __device__ inline int seq_groups(int n, int max_tokens, int window, int
   return len ? (len + kGroup - 1) / kGroup - first / kGroup : 0;
 }
 
-// N groups over at most `ctas` CTAs: CTA c of active_ctas takes [range_start(c), range_start(c + 1)).
-__host__ __device__ inline int active_ctas(int64_t N, int ctas) {
-  const int64_t c = N / kMinGroups;
-  return c < 1 ? 1 : c > ctas ? ctas : (int)c;
+// 64-bit division, on the 32-bit path when both operands fit.
+__host__ __device__ inline int64_t div64(int64_t x, int64_t y) {
+  return ((x | y) >> 31) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
-__host__ __device__ inline int64_t range_start(int64_t N, int C, int c) { return (int64_t)c * N / C; }
-__host__ __device__ inline int range_of(int64_t N, int C, int64_t f) { return (int)(((f + 1) * C - 1) / N); }
 
-// Query operands of one unit: the B fragments of q' and S q' (1024 words per n-block of four heads),
-// then (fK, fQ, Kh, 2^-e) per head.
+// How N groups are cut: `warps` warps of each of `ctas` CTAs, warp W = cta * warps + w of them taking
+// groups [range_start(W), range_start(W + 1)), at least one each.  Few groups go to many CTAs rather
+// than to many warps of few.
+struct Cut {
+  int ctas, warps;
+};
+__host__ __device__ inline Cut cut_of(int64_t N, int ctas, int most_warps) {
+  Cut c;
+  const int64_t w = div64(N + ctas - 1, ctas);
+  c.warps = w < 1 ? 1 : w > most_warps ? most_warps : (int)w;
+  const int64_t n = div64(N, c.warps);
+  c.ctas = n < 1 ? 1 : n > ctas ? ctas : (int)n;
+  return c;
+}
+__host__ __device__ inline int64_t range_start(int64_t N, const Cut& c, int64_t W) { return div64(W * N, (int64_t)c.ctas * c.warps); }
+// the warp whose range holds group f
+__host__ __device__ inline int range_of(int64_t N, const Cut& c, int64_t f) {
+  return (int)div64((f + 1) * ((int64_t)c.ctas * c.warps) - 1, N);
+}
+
+// Query operands of one unit: the B fragments of q' and S q' (1024 words per block), then (fK, fQ, Kh,
+// 2^-e) per head.  Up to four heads (nb = 1): one block, head h hi and lo in columns 2h, 2h + 1.  Up to
+// eight (nb = 2): head h in column h, hi in block 0, lo in block 1.
 __host__ __device__ constexpr int seg_bytes(int nb) { return nb * (4096 + 4 * 16); }
 
 struct PagedArgs {
   int B, Hq, Hkv, g, hgroups;
   int pages, ps;          // of the pool
+  uint64_t gpp_inv;       // ceil(2^64 / groups per page): group / groups per page by one product
   int64_t table_stride;
   int max_tokens, window;
-  int ctas, dyn_smem;
+  int ctas;
   const int32_t* table;
   const int32_t* lens;
   const uint8_t* k_codes;
@@ -51,7 +79,7 @@ struct PagedArgs {
   const float* vc;
   // workspace
   uint32_t* ops;          // [units] query operands
-  float* part;            // [units + ctas][heads] partials
+  float* part;            // [units + ctas x warps][heads] partials
   int64_t* before;        // [B + 1] groups of the sequences before b
   unsigned int* err;
 };

@@ -7,8 +7,7 @@
 //   prep    q' and S q' of every head and their tensor-core operands; the running sum of the lengths
 //   split   the stream over the pages (tq_paged_split.cuh): one CTA per SM over an even share
 //   merge   joins the partials of a head by log-sum-exp and turns o' back with Pi^T
-// Prep and merge read Pi and S (64 KB each) once per CTA, not once per head: a CTA holds its share of
-// the matrix in registers and takes the heads of a unit, or several units, past it.
+// Prep and merge read Pi and S (64 KB each) once per CTA, not once per head.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -25,12 +24,105 @@ namespace {
 // Same bits as the contiguous decode's, and bit 4: a page number or a length out of range.
 __device__ unsigned int g_paged_error;
 
+// -------------------------------------------------------------------------- 128 x 128 products
+//
+// Prep and merge multiply Pi, S and Pi^T with the vectors of up to eight heads.  On the FP32 units such
+// a product is bound by reading the vectors from shared memory (16 us for 512 units of eight heads);
+// here warp w keeps rows 16w .. 16w + 15 of the matrix as m16n8k16 A fragments, fp16 hi + lo of 2^8 M,
+// for all units it meets, and the heads are the 8 columns.  The vectors enter as fp16 hi + lo of x 2^e
+// with max |x| 2^e in [2^10, 2^11): M x = 2^-(8+e) (Mhi xhi + Mhi xlo + Mlo xhi), off by about 2^-22.
+
+constexpr int MT = 256;              // threads: eight warps of 16 rows
+constexpr int VS = D + 4;            // stride of a head's vector in shared memory (no bank conflicts)
+constexpr float M_SCALE = 256.0f;
+
+template <bool LO>
+struct AFrag {
+  uint32_t hi[8][4], lo[LO ? 8 : 1][4];
+  __device__ __forceinline__ void set(int kk, int r, float x, float y) {
+    x *= M_SCALE;
+    y *= M_SCALE;
+    float xh, xl, yh, yl;
+    split_half(x, xh, xl);
+    split_half(y, yh, yl);
+    hi[kk][r] = pack_half2(xh, yh);
+    if constexpr (LO) lo[kk][r] = pack_half2(xl, yl);
+  }
+  // rows 16w + gq (+ 8) of a row-major matrix, columns 16kk + 2t (+ 8), + 1
+  __device__ __forceinline__ void load(const float* M, int w, int gq, int t) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(M + (16 * w + gq + 8 * (r & 1)) * D + 16 * kk + 2 * t + 8 * (r >> 1)));
+        set(kk, r, v.x, v.y);
+      }
+  }
+  // the same of its transpose
+  __device__ __forceinline__ void load_t(const float* M, int w, int gq, int t) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float* m = M + (16 * kk + 2 * t + 8 * (r >> 1)) * D + 16 * w + gq + 8 * (r & 1);
+        set(kk, r, __ldg(m), __ldg(m + D));
+      }
+  }
+};
+
+// A lane's share of its column's vector: x[4kk + 2r + i] = element 16kk + 8r + 2t + i of head gq.
+// Products of the warp's 16 rows with the eight vectors: y[0], y[1]: row gq of heads 2t, 2t + 1, y[2],
+// y[3]: row gq + 8.
+template <bool LO>
+__device__ __forceinline__ void rows_times(const AFrag<LO>& A, const float (&x)[32], float (&y)[4]) {
+  float mx = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
+  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+  int e = ((__float_as_int(mx) >> 23) & 255) - 127;
+  e = e < -100 ? -100 : e > 126 ? 126 : e;  // (infinities and NaN stay what they are)
+  const float up = __int_as_float((127 + 10 - e) << 23);
+  float d[2][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[0][i] = d[1][i] = 0.0f;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    uint32_t bh[2], bl[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float h0, l0, h1, l1;
+      split_half(x[4 * kk + 2 * r] * up, h0, l0);
+      split_half(x[4 * kk + 2 * r + 1] * up, h1, l1);
+      bh[r] = pack_half2(h0, h1);
+      bl[r] = pack_half2(l0, l1);
+    }
+    mma16816(d[0], A.hi[kk], bh[0], bh[1]);
+    mma16816(d[1], A.hi[kk], bl[0], bl[1]);
+    if constexpr (LO) mma16816(d[1], A.lo[kk], bh[0], bh[1]);
+  }
+  const float down = __int_as_float((127 + e - 18) << 23);  // of head gq: 2^(e - 10) / 2^8
+  const int t = threadIdx.x & 3;
+  const float d0 = __shfl_sync(FULL, down, 8 * t), d1 = __shfl_sync(FULL, down, 8 * t + 4);
+  y[0] = (d[0][0] + d[1][0]) * d0;
+  y[1] = (d[0][1] + d[1][1]) * d1;
+  y[2] = (d[0][2] + d[1][2]) * d0;
+  y[3] = (d[0][3] + d[1][3]) * d1;
+}
+__device__ __forceinline__ void lane_share(const float* v, float (&x)[32]) {  // v: the head's vector
+  const int t = threadIdx.x & 3;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 p = *reinterpret_cast<const float2*>(v + 8 * i + 2 * t);
+    x[2 * i] = p.x;
+    x[2 * i + 1] = p.y;
+  }
+}
+
 // ------------------------------------------------------------------------------------------ prep
 
-constexpr int PREP_THREADS = 512;  // four per matrix row
-
 struct PrepArgs {
-  int B, Hq, Hkv, g, hgroups, nb, qjl;
+  int B, Hq, Hkv, g, hgroups, nb;
   int units, max_tokens, window;
   float sK, sQ;
   const void* q;
@@ -43,39 +135,23 @@ struct PrepArgs {
   unsigned int* err;
 };
 
-__device__ __forceinline__ void load_quarter(const float* M, int j, int q, float4 (&m)[8]) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m[k] = __ldg(reinterpret_cast<const float4*>(M + j * D) + q + 4 * k);
-}
-__device__ __forceinline__ float dot_quarter(const float4 (&m)[8], const float* x, int q) {
-  const float4* v = reinterpret_cast<const float4*>(x) + q;
-  float a0 = 0.0f, a1 = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float4 w = v[4 * k];
-    a0 = fmaf(m[k].x, w.x, a0);
-    a1 = fmaf(m[k].y, w.y, a1);
-    a0 = fmaf(m[k].z, w.z, a0);
-    a1 = fmaf(m[k].w, w.w, a1);
-  }
-  float acc = a0 + a1;
-  acc += __shfl_xor_sync(FULL, acc, 1);
-  return acc + __shfl_xor_sync(FULL, acc, 2);
-}
-
-__global__ void __launch_bounds__(PREP_THREADS, 1) paged_prep(const __grid_constant__ PrepArgs a) {
-  __shared__ float xs[HG][D], qs[HG][D], ss[HG][D];
+template <bool QJL>
+__global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ PrepArgs a) {
+  __shared__ float qs[HG][VS], ss[HG][VS];
   __shared__ float4 hc[HG];
-  __shared__ int64_t wsum[PREP_THREADS / 32];
+  __shared__ int64_t wsum[MT / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if (blockIdx.x == gridDim.x - 1) {
     // the last CTA: groups of the sequences before each one
     if (tid == 0) *a.err = 0u;
     int64_t base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += PREP_THREADS) {
+    bool bad = false;
+    for (int b0 = 0; b0 < a.B; b0 += MT) {
       int first, len;
-      int64_t x = b0 + tid < a.B ? seq_groups(a.lens[b0 + tid], a.max_tokens, a.window, first, len) : 0;
+      const int n = b0 + tid < a.B ? a.lens[b0 + tid] : 0;
+      bad = bad || n < 0 || n > a.max_tokens;
+      int64_t x = seq_groups(n, a.max_tokens, a.window, first, len);
       const int64_t own = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -86,7 +162,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) paged_prep(const __grid_const
       if (lane == 31) wsum[warp] = x;
       __syncthreads();
       int64_t low = 0, all = 0;
-      for (int w = 0; w < PREP_THREADS / 32; ++w) {
+      for (int w = 0; w < MT / 32; ++w) {
         low += w < warp ? wsum[w] : 0;
         all += wsum[w];
       }
@@ -94,31 +170,61 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) paged_prep(const __grid_const
       base += all;
     }
     if (tid == 0) a.before[a.B] = base;
+    if (bad) atomicOr(a.err, 16u);  // (after the barriers that follow its clearing)
     return;
   }
-  const int j = tid >> 2, q = tid & 3, hgn = 4 * a.nb, ctas = gridDim.x - 1;
+  const int gq = lane >> 2, t = lane & 3, hgn = 4 * a.nb, ctas = gridDim.x - 1;
   const int seg_words = seg_bytes(a.nb) / 4;
-  float4 pm[8], sm[8];
-  load_quarter(a.Pi, j, q, pm);
-  if (a.qjl) load_quarter(a.S, j, q, sm);
-  for (int u = blockIdx.x; u < a.units; u += ctas) {
-    const int hg = u % a.hgroups, kvh = (u / a.hgroups) % a.Hkv, b = u / (a.hgroups * a.Hkv);
-    const int nh = min(HG, a.g - hg * HG);
-    const int64_t q0 = ((int64_t)b * a.Hq + (int64_t)kvh * a.g + hg * HG) * D;
-    for (int i = tid; i < nh * D; i += PREP_THREADS)
-      (&xs[0][0])[i] = a.q_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.q)[q0 + i])
-                                : reinterpret_cast<const float*>(a.q)[q0 + i];
-    __syncthreads();
-    for (int h = 0; h < nh; ++h) {
-      const float y = dot_quarter(pm, xs[h], q);
-      if (q == (h & 3)) qs[h][j] = y;
-    }
-    __syncthreads();
-    if (a.qjl) {
-      for (int h = 0; h < nh; ++h) {
-        const float y = dot_quarter(sm, qs[h], q);
-        if (q == (h & 3)) ss[h][j] = y;
+  // this lane's share of head gq of unit u (0 past the unit's heads)
+  auto load_q = [&](int u, float (&x)[32]) {
+    const int hg = u % a.hgroups, bk = u / a.hgroups;
+    const bool live = u < a.units && gq < min(HG, a.g - hg * HG);
+    const int64_t at = ((int64_t)bk * a.g + hg * HG + gq) * D + 2 * t;
+    if (!live) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+    } else if (a.q_bf16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + at + 8 * i));
+        x[2 * i] = __uint_as_float(w << 16);
+        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 w = __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(a.q) + at + 8 * i));
+        x[2 * i] = w.x;
+        x[2 * i + 1] = w.y;
+      }
+    }
+  };
+  float next[32];
+  load_q(blockIdx.x, next);
+  AFrag<true> pi;
+  AFrag<false> sk;
+  pi.load(a.Pi, warp, gq, t);
+  if constexpr (QJL) sk.load(a.S, warp, gq, t);  // (entries exact in fp16)
+  for (int u = blockIdx.x; u < a.units; u += ctas) {
+    const int hg = u % a.hgroups, nh = min(HG, a.g - hg * HG);
+    float x[32], y[4];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = next[i];
+    load_q(u + ctas, next);
+    rows_times(pi, x, y);
+    const int row = 16 * warp + gq;
+    qs[2 * t][row] = y[0];
+    qs[2 * t + 1][row] = y[1];
+    qs[2 * t][row + 8] = y[2];
+    qs[2 * t + 1][row + 8] = y[3];
+    __syncthreads();
+    if constexpr (QJL) {
+      lane_share(qs[gq], x);
+      rows_times(sk, x, y);
+      ss[2 * t][row] = y[0];
+      ss[2 * t + 1][row] = y[1];
+      ss[2 * t][row + 8] = y[2];
+      ss[2 * t + 1][row + 8] = y[3];
       __syncthreads();
     }
     // per head: a power of two 2^-e that brings q' and 16 S q' below 2^14 (fp16 range), and the QJL
@@ -131,13 +237,13 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) paged_prep(const __grid_const
       } else {
         float mx = 0.0f;
 #pragma unroll
-        for (int k = lane; k < D; k += 32) mx = fmaxf(mx, fmaxf(fabsf(qs[h][k]), a.qjl ? 16.0f * fabsf(ss[h][k]) : 0.0f));
+        for (int k = lane; k < D; k += 32) mx = fmaxf(mx, fmaxf(fabsf(qs[h][k]), QJL ? 16.0f * fabsf(ss[h][k]) : 0.0f));
 #pragma unroll
         for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
         const int ex = (mx < 16384.0f || !(mx < INFINITY)) ? 0 : ((__float_as_int(mx) >> 23) & 255) - 127 - 13;
         const float dn = __int_as_float((127 - ex) << 23);
         float ch = 0.0f, sh = 0.0f;
-        if (a.qjl) {
+        if constexpr (QJL) {
 #pragma unroll
           for (int k = lane; k < D; k += 32) {
             const float scl = (float)(16 >> ((k >> 3) & 3));  // sgn_scale of the k-step pair
@@ -160,42 +266,44 @@ __global__ void __launch_bounds__(PREP_THREADS, 1) paged_prep(const __grid_const
       }
     }
     __syncthreads();
-    // Fragments: column gq of n-block nb is head 4 nb + gq / 2, part gq % 2 (0: fp16 hi, 1: lo); k-step
-    // kk holds k = 16kk + 2t, +1 (register 0), +8, +9 (register 1) of lane (gq, t).  Word 2kk + r of a
-    // lane is q', word 16 + 2kk + r is S q'; stored [n-block][word / 4][lane][word % 4].
-    uint32_t* dst = a.ops + (int64_t)u * seg_words;
-    for (int i = tid; i < a.nb * 1024; i += PREP_THREADS) {
-      const int word = ((i >> 7) & 7) * 4 + (i & 3), ln = (i >> 2) & 31, nb = i >> 10;
-      const int kk = (word >> 1) & 7, r = word & 1, sq = word >> 4;
-      const int h = 4 * nb + (ln >> 3), t = ln & 3;
-      const bool lo = (ln >> 2) & 1;
-      uint32_t v = 0u;
-      if (h < nh && (!sq || a.qjl)) {
-        const float* src = (sq ? ss[h] : qs[h]) + 16 * kk + 8 * r + 2 * t;
-        const float f = hc[h].w * (sq ? sgn_scale(2 * kk + r) : 1.0f);
-        float h0, l0, h1, l1;
-        split_half(src[0] * f, h0, l0);
-        split_half(src[1] * f, h1, l1);
-        v = lo ? pack_half2(l0, l1) : pack_half2(h0, h1);
+    // Fragments: columns as seg_bytes says; k-step kk holds k = 16kk + 2t, + 1 (register 0), + 8, + 9
+    // (register 1) of lane (gq, t).  Word 2kk + r of a lane is q', word 16 + 2kk + r is S q'; stored
+    // [block][word / 4][lane][word % 4].
+    uint4* dst = reinterpret_cast<uint4*>(a.ops + (int64_t)u * seg_words);
+    for (int i = tid; i < a.nb * 256; i += MT) {
+      const int w4 = (i >> 5) & 7, ln = i & 31, nb = i >> 8, sq = w4 >> 2;
+      const int h = a.nb == 1 ? ln >> 3 : ln >> 2;
+      const bool lo = a.nb == 1 ? (ln >> 2) & 1 : nb;
+      uint32_t v[4] = {0u, 0u, 0u, 0u};
+      if (h < nh && (!sq || QJL)) {
+        const float* src = (sq ? ss[h] : qs[h]) + 32 * (w4 & 3) + 2 * (ln & 3);
+        const float dn = hc[h].w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // k-steps 2 (w4 % 4) and + 1, both registers
+          const float f = dn * (sq ? sgn_scale(j) : 1.0f);
+          float h0, l0, h1, l1;
+          split_half(src[8 * j] * f, h0, l0);
+          split_half(src[8 * j + 1] * f, h1, l1);
+          v[j] = lo ? pack_half2(l0, l1) : pack_half2(h0, h1);
+        }
       }
-      dst[i] = v;
+      dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
     }
-    if (tid < hgn) reinterpret_cast<float4*>(dst + a.nb * 1024)[tid] = hc[tid];
+    if (tid < hgn) reinterpret_cast<float4*>(dst + a.nb * 256)[tid] = hc[tid];
     __syncthreads();  // the next unit reuses the vectors
   }
 }
 
 // ------------------------------------------------------------------------------------------ merge
 //
-// A CTA of 1024 threads (d = tid % 128, q = tid / 128) takes HPC heads of one unit: all of them, so
-// that Pi is read once per unit, or one when there are too few units to fill the SMs.  With one head
-// the eight thread groups share its partials; with several, group q joins head q's.  The turn back
-// o_i = sum_j Pi[j][i] o'_j gives thread (i, q) rows 16q .. 16q + 15, loaded before the wait.
+// A CTA joins the partials of all heads of a unit (warp h those of head h) or, when there are too few
+// units to fill the SMs, of one head (the warps share its partials), and turns the joined o' back:
+// o_i = sum_j Pi[j][i] o'_j, with Pi^T loaded before the wait for the split kernel.
 
-constexpr int MG = 8, MERGE_T = MG * D, MROWS = D / MG;
+constexpr int MW = MT / 32;
 
 struct MergeArgs {
-  int B, Hq, Hkv, g, hgroups, hgn, ctas;
+  int B, Hq, Hkv, g, hgroups, hgn, ctas, warps, items;
   const float* part;
   const int64_t* before;
   const float* Pi;
@@ -205,99 +313,110 @@ struct MergeArgs {
   float* lse;
 };
 
-__device__ __forceinline__ void put_out(const MergeArgs& a, int64_t i, float v) {
-  if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(v);
-  else reinterpret_cast<float*>(a.out)[i] = v;
-}
-
 template <bool ONE>
-__global__ void __launch_bounds__(MERGE_T) paged_merge(const __grid_constant__ MergeArgs a) {
-  __shared__ float ob[HG][D];             // joined o' of each head
-  __shared__ float red[MG][ONE ? 3 : HG][D];
-  const int tid = threadIdx.x, d = tid % D, q = tid / D;
-  float pj[MROWS];
-#pragma unroll
-  for (int r = 0; r < MROWS; ++r) pj[r] = __ldg(a.Pi + (MROWS * q + r) * D + d);
+__global__ void __launch_bounds__(MT) paged_merge(const __grid_constant__ MergeArgs a) {
+  __shared__ float os[HG][VS];              // joined o' of each head
+  __shared__ float rm[MW], rl[MW], ro[ONE ? MW : 1][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, t = lane & 3;
+  AFrag<true> pt;
+  pt.load_t(a.Pi, warp, gq, t);
+  for (int i = tid; i < HG * VS; i += MT) (&os[0][0])[i] = 0.0f;  // columns without a head
+  __syncthreads();
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (blockIdx.x == 0 && tid == 0 && *a.err) atomicOr(&g_paged_error, *a.err);
-  const int u = ONE ? blockIdx.x / a.hgn : blockIdx.x;
-  const int U = a.Hkv * a.hgroups, b = u / U, uu = u % U;
-  const int hg = uu % a.hgroups, kvh = uu / a.hgroups;
-  const int nh = min(HG, a.g - hg * HG);
-  const int h0 = ONE ? blockIdx.x % a.hgn : 0;
-  if (ONE && h0 >= nh) return;
-  const int64_t orow = (int64_t)b * a.Hq + (int64_t)kvh * a.g + hg * HG;
-  const int64_t lo = __ldcg(a.before + b), G = __ldcg(a.before + b + 1) - lo, N = __ldcg(a.before + a.B) * U;
-  if (G == 0) {
-    for (int h = ONE ? h0 : q; h < (ONE ? h0 + 1 : nh); h += MG) {
-      if (ONE && q) break;
-      put_out(a, (orow + h) * D + d, 0.0f);
-      if (a.lse && d == 0) a.lse[orow + h] = -INFINITY;
+  const int U = a.Hkv * a.hgroups;
+  const int64_t N = __ldcg(a.before + a.B) * U;
+  const Cut cut = cut_of(N, a.ctas, a.warps);
+  for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
+    const int u = ONE ? item / a.hgn : item, h0 = ONE ? item % a.hgn : 0;
+    const int b = u / U, uu = u - b * U, hg = uu % a.hgroups, kvh = uu / a.hgroups;
+    const int nh = min(HG, a.g - hg * HG);
+    if (ONE && h0 >= nh) continue;
+    const int64_t orow = (int64_t)b * a.Hq + (int64_t)kvh * a.g + hg * HG;
+    const int64_t lo = __ldcg(a.before + b), G = __ldcg(a.before + b + 1) - lo;
+    // Partials: the unit's own record (of the warp, or the joint CTA, that opens it), then those of the
+    // warps that go on with it: in the CTA where the unit opens, one for each CTA inside the unit, and in
+    // the CTA where it ends (one if that CTA ends with it).
+    int S = 0, w0 = 0, c0 = 0, c1 = 0, in0 = 0, mid = 0;
+    if (G > 0) {
+      const int64_t f0 = lo * U + (int64_t)uu * G, f1 = f0 + G;
+      w0 = range_of(N, cut, f0);
+      const int w1 = range_of(N, cut, f1 - 1);
+      c0 = w0 / cut.warps;
+      c1 = w1 / cut.warps;
+      const bool joint0 = range_start(N, cut, (int64_t)c0 * cut.warps) == f0 && range_start(N, cut, (int64_t)(c0 + 1) * cut.warps) <= f1;
+      in0 = joint0 ? 0 : min(w1, (c0 + 1) * cut.warps - 1) - w0;
+      mid = max(0, c1 - c0 - 1);
+      S = 1 + in0 + mid;
+      if (c1 > c0) S += range_start(N, cut, (int64_t)(c1 + 1) * cut.warps) == f1 ? 1 : w1 - c1 * cut.warps + 1;
     }
-    return;
-  }
-  const int C = active_ctas(N, a.ctas);
-  const int64_t f0 = lo * U + (int64_t)uu * G;
-  const int c0 = range_of(N, C, f0), c1 = range_of(N, C, f0 + G - 1);
-  // partials: the unit's own record, then those of the CTAs that go on with it
-  const int S = 1 + c1 - c0;
-  auto record = [&](int s, int h) {
-    const int64_t slot = s == 0 ? u : (int64_t)a.B * U + c0 + s;
-    return a.part + (slot * a.hgn + h) * PART;
-  };
-  float M = -1e30f, L = 0.0f, O = 0.0f;
-  const int h = ONE ? h0 : q;
-  if (ONE || q < nh) {
+    auto slot_of = [&](int s) -> int64_t {
+      if (s == 0) return u;
+      const int W = s <= in0 ? w0 + s : s <= in0 + mid ? (c0 + s - in0) * cut.warps : c1 * cut.warps + s - 1 - in0 - mid;
+      return (int64_t)a.B * U + W;
+    };
+    const int h = ONE ? h0 : warp;
+    float M = -1e30f, L = 0.0f;
+    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (h < nh) {
 #pragma unroll 4
-    for (int s = ONE ? q : 0; s < S; s += ONE ? MG : 1) {
-      const float* p = record(s, h);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
-      const float o = __ldcg(p + 4 + d);
-      const float Mn = fmaxf(M, ml.x);
-      const float w0 = ex2(M - Mn), w1 = ex2(ml.x - Mn);
-      L = fmaf(w1, ml.y, L * w0);
-      O = fmaf(w1, o, O * w0);
-      M = Mn;
-    }
-  }
-  if constexpr (ONE) {
-    red[q][0][d] = M;
-    red[q][1][d] = L;
-    red[q][2][d] = O;
-    __syncthreads();
-    if (q == 0) {
-#pragma unroll
-      for (int k = 0; k < MG; ++k) M = fmaxf(M, red[k][0][d]);
-      L = 0.0f;
-      O = 0.0f;
-#pragma unroll
-      for (int k = 0; k < MG; ++k) {
-        const float w = ex2(red[k][0][d] - M);
-        L = fmaf(w, red[k][1][d], L);
-        O = fmaf(w, red[k][2][d], O);
+      for (int s = ONE ? warp : 0; s < S; s += ONE ? MW : 1) {
+        const float* p = a.part + (slot_of(s) * a.hgn + h) * PART;
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+        const float Mn = fmaxf(M, ml.x);
+        const float w0 = ex2(M - Mn), w1 = ex2(ml.x - Mn);
+        L = fmaf(w1, ml.y, L * w0);
+        O.x = fmaf(w1, o.x, O.x * w0);
+        O.y = fmaf(w1, o.y, O.y * w0);
+        O.z = fmaf(w1, o.z, O.z * w0);
+        O.w = fmaf(w1, o.w, O.w * w0);
+        M = Mn;
       }
     }
+    if constexpr (ONE) {
+      if (lane == 0) {
+        rm[warp] = M;
+        rl[warp] = L;
+      }
+      *reinterpret_cast<float4*>(&ro[warp][4 * lane]) = O;
+      __syncthreads();
+      if (warp == 0) {
+        O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        L = 0.0f;
+#pragma unroll
+        for (int k = 0; k < MW; ++k) M = fmaxf(M, rm[k]);
+#pragma unroll
+        for (int k = 0; k < MW; ++k) {
+          const float w = ex2(rm[k] - M);
+          const float4 o = *reinterpret_cast<const float4*>(&ro[k][4 * lane]);
+          L = fmaf(w, rl[k], L);
+          O.x = fmaf(w, o.x, O.x);
+          O.y = fmaf(w, o.y, O.y);
+          O.z = fmaf(w, o.z, O.z);
+          O.w = fmaf(w, o.w, O.w);
+        }
+      }
+    }
+    if (h < nh && (!ONE || warp == 0)) {
+      const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+      *reinterpret_cast<float4*>(&os[ONE ? 0 : h][4 * lane]) = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+      if (a.lse && lane == 0) a.lse[orow + h] = S ? M * 0.69314718055994531f + logf(L) : -INFINITY;
+    }
     __syncthreads();
-  }
-  if (ONE ? q == 0 : q < nh) {
-    ob[ONE ? 0 : q][d] = L != 0.0f ? O / L : 0.0f;
-    if (a.lse && d == 0) a.lse[orow + h] = M * 0.69314718055994531f + logf(L);
-  }
-  __syncthreads();
+    float x[32], y[4];
+    lane_share(os[gq], x);
+    rows_times(pt, x, y);
 #pragma unroll
-  for (int x = 0; x < (ONE ? 1 : HG); ++x) {
-    if (!ONE && x >= nh) break;
-    float r = 0.0f;
-#pragma unroll
-    for (int k = 0; k < MROWS; ++k) r = fmaf(pj[k], ob[x][MROWS * q + k], r);
-    red[q][x][d] = r;
-  }
-  __syncthreads();
-  if (ONE ? q == 0 : q < nh) {
-    float r = 0.0f;
-#pragma unroll
-    for (int k = 0; k < MG; ++k) r += red[k][ONE ? 0 : q][d];
-    put_out(a, (orow + h) * D + d, r);
+    for (int i = 0; i < 4; ++i) {
+      const int col = 2 * t + (i & 1);
+      if (ONE ? col == 0 : col < nh) {
+        const int64_t at = (orow + (ONE ? h0 : col)) * D + 16 * warp + gq + 8 * (i >> 1);
+        if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y[i]);
+        else reinterpret_cast<float*>(a.out)[at] = y[i];
+      }
+    }
+    __syncthreads();  // the next item reuses the vectors
   }
 }
 
@@ -326,7 +445,7 @@ WsPlan ws_plan(int B, int Hq, int Hkv, int ctas) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   w.ops = 0;
   w.part = up((size_t)w.units * seg_bytes(w.nb));
-  w.before = w.part + up((size_t)(w.units + ctas) * 4 * w.nb * PART * 4);
+  w.before = w.part + up((size_t)(w.units + ctas * paged_warps(w.nb)) * 4 * w.nb * PART * 4);
   w.err = w.before + up((size_t)(B + 1) * 8);
   w.bytes = w.err + 256;
   return w;
@@ -411,11 +530,13 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   a.hgroups = w.hgroups;
   a.pages = pool->B;
   a.ps = pool->T_cap;
+  // exact for every group number below 2^32 / groups per page and far beyond (2^64 / d rounded up is off by
+  // less than d / 2^64 relative)
+  a.gpp_inv = ~0ull / (uint64_t)(pool->T_cap / kGroup) + 1;
   a.table_stride = table_stride;
   a.max_tokens = max_pages * pool->T_cap;
   a.window = window;
   a.ctas = sms;
-  a.dyn_smem = attr_of(cudaDevAttrMaxSharedMemoryPerBlockOptin, 232448) / 256 * 256;
   a.table = table;
   a.lens = seq_lens;
   a.k_codes = pool->k_codes;
@@ -438,12 +559,12 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   p.g = a.g;
   p.hgroups = w.hgroups;
   p.nb = w.nb;
-  p.qjl = pool->qjl_m ? 1 : 0;
+  const bool qjl = pool->qjl_m != 0;
   p.units = (int)w.units;
   p.max_tokens = a.max_tokens;
   p.window = window;
   p.sK = (float)(sc / sqrt((double)D));
-  p.sQ = p.qjl ? (float)(sc * 2.0 * sqrt(M_PI / 2.0) / pool->qjl_m) : 0.0f;
+  p.sQ = qjl ? (float)(sc * 2.0 * sqrt(M_PI / 2.0) / pool->qjl_m) : 0.0f;
   p.q = q;
   p.q_bf16 = q_dtype == TQ_BF16;
   p.Pi = params->Pi;
@@ -452,9 +573,8 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   p.ops = a.ops;
   p.before = a.before;
   p.err = a.err;
-  st = launch_dep(paged_prep, std::min<int64_t>(w.units, sms - 1) + 1, PREP_THREADS, s, false, "paged prep", p);
+  st = launch_dep(qjl ? paged_prep<true> : paged_prep<false>, std::min<int64_t>(w.units, sms - 1) + 1, MT, s, false, "paged prep", p);
   if (st != TQ_OK) return st;
-  const bool qjl = p.qjl != 0;
   st = pool->k_bits == 2   ? paged_split_k2(a, pool->v_bits, qjl, s)
        : pool->k_bits == 3 ? paged_split_k3(a, pool->v_bits, qjl, s)
                            : paged_split_k4(a, pool->v_bits, qjl, s);
@@ -467,6 +587,7 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   m.hgroups = w.hgroups;
   m.hgn = 4 * w.nb;
   m.ctas = sms;
+  m.warps = paged_warps(w.nb);
   m.part = a.part;
   m.before = a.before;
   m.Pi = params->Pi;
@@ -474,7 +595,8 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   m.out = out;
   m.out_bf16 = out_dtype == TQ_BF16;
   m.lse = lse;
-  // one head per CTA while the units alone would leave SMs idle
-  if (w.units < sms) return launch_dep(paged_merge<true>, w.units * m.hgn, MERGE_T, s, true, "paged merge", m);
-  return launch_dep(paged_merge<false>, w.units, MERGE_T, s, true, "paged merge", m);
+  // one head per CTA while the units alone would leave SMs idle; two CTAs fit an SM
+  const bool one = w.units < sms;
+  m.items = (int)(one ? w.units * m.hgn : w.units);
+  return launch_dep(one ? paged_merge<true> : paged_merge<false>, std::min<int64_t>(m.items, 2 * sms), MT, s, true, "paged merge", m);
 }

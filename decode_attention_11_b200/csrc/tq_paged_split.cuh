@@ -2,25 +2,32 @@
 //
 // Work.  The tokens a sequence shows (all, or a window's) are cut into groups of 16, which never cross
 // a page.  The groups of all units -- a unit is one (sequence, kv-head) and up to eight of its query
-// heads -- are laid end to end and cut into one even, contiguous range per CTA, so ragged batches
-// load every SM alike.  The cut follows from the lengths on the device: every CTA sums them itself.
-// A range is processed as segments, each inside one unit; a segment ends with one (max, sum, o')
-// partial per head, which the merge kernel joins.
+// heads -- are laid end to end and cut into one even, contiguous range per warp, so ragged batches
+// load every warp alike.  The cut follows from the lengths on the device: every CTA sums them itself.
+// A warp's range is processed as segments, each inside one unit; a segment ends with one
+// (max, sum, o') partial per head, which the merge kernel joins.  A CTA whose whole range lies in one
+// unit (long contexts) joins its warps first, so that a long unit leaves one partial per CTA.
 //
-// CTA.  One producer warp and NW consumer warps.  The producer walks the segments: it looks up the
-// pages of a stage (one group per consumer warp) one stage ahead, and moves each run of groups inside
-// a page with one bulk copy per cache array into a ring of shared-memory slots, and each segment's
-// query operands (built by the prep kernel) into a double buffer, all completing on mbarriers.  It
-// needs no query, so the ring fills while the prep kernel still runs (programmatic dependent
-// launch).  A consumer warp turns 16 tokens of every stage into tensor-core operands:
-//   scores   D[16 tokens x 8] += A[tokens x dims] B[dims x (4 heads, fp16 hi and lo)]: A are centroid
-//            pairs from a lane-replicated shared-memory table; a second product with the sign bits
-//            placed in fp16 mantissas gives the QJL term
-//   values   O'^T[16 dims x 8] += A[dims x tokens] B[tokens x (4 heads, hi and lo)]: A are centroid
-//            pairs of two tokens, B the weights p ||v|| / sqrt(128)
+// Warps run on their own: each keeps a ring of DEPTH groups in shared memory and fetches its next
+// groups itself with 16-byte cp.async (five per lane and group), pages looked up one group ahead.
+// (One producer warp with bulk copies per page, an mbarrier ring and CTA-wide segments measured 134 us
+// at 16 sequences x 16K tokens in 4 bits with pages of 64, against 97 us of the same bytes with pages
+// of 128: it was bound by issuing the copies, and short sequences by the barriers at their ends.)
+// Nothing before the first product needs a query, so the rings fill while the prep kernel still runs
+// (programmatic dependent launch).  16 tokens become tensor-core operands:
+//   scores   D[16 tokens x 8] += A[tokens x dims] B[dims x 8]: A are centroid pairs from a
+//            lane-replicated shared-memory table; a second product with the sign bits placed in fp16
+//            mantissas gives the QJL term
+//   values   O'^T[16 dims x 8] += A[dims x tokens] B[tokens x 8]: A are centroid pairs of two tokens, B
+//            the weights p ||v|| / sqrt(128)
 // with online softmax in log2 units in between.  q' and the weights enter as fp16 hi + lo (about 22
-// bits), sums are fp32.  Rows outside the tokens shown are masked by selection, never by a product,
-// so whatever they hold (NaN too) stays out.
+// bits), sums are fp32.  The 8 columns of B are four heads, hi and lo side by side (one product), or,
+// for five to eight heads, eight heads, hi and lo in two products onto the same sums: that keeps the
+// sums at 32 registers.  The running maximum moves only when a score passes it by more than
+// LAZY (a vote instead of a three-step exchange per group): weights reach 2^LAZY, which the value scale
+// takes back so that they stay as far inside fp16 range as weights of at most 1.
+// Rows outside the tokens shown are masked by selection, never by a product, so whatever they hold
+// (NaN too) stays out.
 #pragma once
 
 #include <algorithm>
@@ -31,616 +38,629 @@
 namespace tq {
 namespace {
 
-template <int NB>
-struct PShape {
-  // Registers split between the SM's four schedulers: 12 warps leave 168 a thread, enough for one
-  // n-block of four heads; two n-blocks need up to 255 and run with 8 warps.
-  static constexpr int NW = NB == 1 ? 11 : 7;
-  static constexpr int THREADS = 32 * (NW + 1);
-};
-constexpr int P_NS_MAX = 8;
-constexpr long long P_WAIT_LIMIT = 4000000000LL;  // ~2 s of SM clock per wait
+constexpr float LAZY = 4.0f;
+constexpr float LAZY_SCALE = 1.0f / 16.0f;  // 2^-LAZY
+constexpr int P_LENS = 512;                 // sequences whose lengths and running sums are kept in shared memory
+constexpr int P_SMEM = 232448;              // dynamic shared memory of a CTA (all an SM gives one)
+constexpr int P_MISC = 8192;                // lengths, sums, codebooks
 
-// What the producer tells the consumers of a segment.
-struct Seg {
-  int32_t n;         // groups; 0: the range is done
-  int32_t tok0;      // first token of the first group
-  int32_t first, len;  // tokens shown: [first, len)
-  int64_t slot;      // partial record
-};
-
-struct PCtrl {
-  uint64_t full[P_NS_MAX], empty[P_NS_MAX];
-  uint64_t sfull[2], sempty[2];
-  Seg seg[2];
-  uint32_t stage_off[P_NS_MAX];
-  uint32_t tbl_addr, seg_off, merge_off;
-  int ns;
-  unsigned int err;
-};
-constexpr int P_CTRL_BYTES = 384;
-static_assert(sizeof(PCtrl) <= P_CTRL_BYTES, "control block");
-
+// NB: 1 for up to four heads per unit, 2 for up to eight.
 template <int KB, int VB, bool QJL, int NB>
 struct PLayout {
-  static constexpr int NW = PShape<NB>::NW, ST = 16 * NW, HGN = 4 * NB;
+  static constexpr int NW = paged_warps(NB), THREADS = 32 * NW, HGN = 4 * NB;
   static constexpr int K_ROW = 16 * KB, V_ROW = 16 * VB;
+  // a group in the ring
   static constexpr int OFF_KC = 0;
-  static constexpr int OFF_SG = OFF_KC + ST * K_ROW;
-  static constexpr int OFF_VC = OFF_SG + (QJL ? ST * 16 : 0);
-  static constexpr int OFF_NK = OFF_VC + ST * V_ROW;
-  static constexpr int OFF_RN = OFF_NK + ST * 4;
-  static constexpr int OFF_NV = OFF_RN + (QJL ? ST * 4 : 0);
-  static constexpr int STAGE_BYTES = (OFF_NV + ST * 4 + 127) / 128 * 128;
-  static constexpr int TX_PER_TOKEN = K_ROW + V_ROW + 8 + (QJL ? 20 : 0);
+  static constexpr int OFF_VC = OFF_KC + 16 * K_ROW;
+  static constexpr int OFF_SG = OFF_VC + 16 * V_ROW;
+  static constexpr int OFF_NK = OFF_SG + (QJL ? 256 : 0);
+  static constexpr int OFF_NV = OFF_NK + 64;
+  static constexpr int OFF_RN = OFF_NV + 64;
+  static constexpr int SLOT = OFF_RN + (QJL ? 64 : 0);
+  // Pair tables: 4/4 bits: 256 entries of 256 bytes (key replicas at +0, value replicas at +128) at a
+  // 64 KB boundary of the shared window, so that one byte permute makes an address of a byte of codes;
+  // other widths: 128-byte entries, each table at a multiple of its size (the larger first), so that an
+  // address is a shifted field of codes or'ed into the lane's address of entry 0.
   static constexpr bool kPacked = KB == 4 && VB == 4;
-  static constexpr int K_TBL = kPacked ? 0 : (1 << (2 * KB)) * 128;
-  static constexpr int V_TBL = kPacked ? 0 : (1 << (2 * VB)) * 128;
-  static constexpr int TBL_BYTES = kPacked ? 65536 : K_TBL + V_TBL;
-  static constexpr int SEG_BYTES = seg_bytes(NB);            // a segment's operands, twice
-  // warps' partials of a segment, one n-block at a time: (max, sum) and o' of four heads per warp
-  static constexpr int MERGE_BYTES = 4 * (NW * 4 * 2 + NW * 4 * D);
-  static_assert(STAGE_BYTES % 16 == 0 && OFF_NK % 16 == 0 && OFF_RN % 16 == 0 && OFF_NV % 16 == 0, "bulk copies");
+  static constexpr int K_TBL = (1 << (2 * KB)) * 128, V_TBL = (1 << (2 * VB)) * 128;
+  static constexpr int TBL_BYTES = K_TBL + V_TBL;
+  static constexpr int TBL_ALIGN = kPacked ? 65536 : K_TBL > V_TBL ? K_TBL : V_TBL;
+  // Rings of the warps, before the tables (the first 1 KB of the window is the system's) and behind them.
+  static constexpr int FRONT = TBL_ALIGN > 1024 ? TBL_ALIGN - 1024 : 0;
+  static constexpr int BACK = P_SMEM - P_MISC - TBL_BYTES - FRONT - 1024;
+  static constexpr int rings(int depth) { return FRONT / (depth * SLOT) + BACK / (depth * SLOT); }
+  static constexpr int depth() {
+    int d = 6;
+    while (d > 2 && rings(d) < NW) --d;
+    return d;
+  }
+  static constexpr int DEPTH = depth();
+  static_assert(rings(DEPTH) >= NW, "shared memory");
+  static_assert(SLOT % 16 == 0, "16-byte copies");
 };
 
-// Shared memory: pair tables (at a 64 KB boundary of the window when packed), then first-fit around
-// them the segment operands, the merge area and as many ring slots as fit.
-template <int KB, int VB, bool QJL, int NB>
-__device__ void place_smem(uint32_t base, int dyn, PCtrl& c) {
-  using Lay = PLayout<KB, VB, QJL, NB>;
-  const uint32_t end = base + (uint32_t)dyn - P_CTRL_BYTES;
-  const uint32_t tbl = Lay::kPacked ? ((base + 0xFFFFu) & ~0xFFFFu) : base;
-  uint32_t r0 = base, r1 = tbl + Lay::TBL_BYTES;
-  auto take = [&](uint32_t bytes, uint32_t& off) {
-    bytes = (bytes + 127u) & ~127u;
-    if (tbl - r0 >= bytes) {
-      off = r0 - base;
-      r0 += bytes;
-      return true;
-    }
-    if (r1 <= end && end - r1 >= bytes) {
-      off = r1 - base;
-      r1 += bytes;
-      return true;
-    }
-    return false;
-  };
-  c.tbl_addr = tbl;
-  c.ns = 0;
-  if (r1 > end || !take(Lay::MERGE_BYTES, c.merge_off) || !take(2 * Lay::SEG_BYTES, c.seg_off)) return;
-  int ns = 0;
-  while (ns < P_NS_MAX && take(Lay::STAGE_BYTES, c.stage_off[ns])) ++ns;
-  c.ns = ns >= 2 ? ns : 0;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ bool pwait(PCtrl& c, uint64_t* bar, uint32_t parity) {
-  const uint32_t addr = smem_u32(bar);
-  const long long t0 = clock64();
-  while (true) {
-    if (__any_sync(FULL, mbar_try(addr, parity))) return true;
-    const bool stop = (*reinterpret_cast<volatile unsigned int*>(&c.err) & 3u) != 0 || clock64() - t0 > P_WAIT_LIMIT;
-    if (__any_sync(FULL, stop)) {
-      if ((threadIdx.x & 31) == 0) atomicOr(&c.err, 1u);
-      return false;
+template <int OFF>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1], 16;\n" ::"r"(dst), "l"(src), "n"(OFF) : "memory");
+}
+// Loads of a group's rows (after its wait: volatile) ...
+template <int OFF>
+__device__ __forceinline__ uint32_t ld32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1 + %2];\n" : "=r"(v) : "r"(p), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ float ldf(uint32_t p) { return __uint_as_float(ld32<OFF>(p)); }
+template <int OFF>
+__device__ __forceinline__ uint2 ld64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];\n" : "=r"(v.x), "=r"(v.y) : "r"(p), "n"(OFF));
+  return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint4 ld128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p), "n"(OFF));
+  return v;
+}
+// ... and of the tables, which do not change; their order and the products' is the compiler's.
+__device__ __forceinline__ uint32_t lut32(uint32_t p) {
+  uint32_t v;
+  asm("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// Table entry of the W-bit field at bit POS of a code stream: r is the lane's address of entry 0.
+// PACKED: W = 8 and 256-byte entries (see PLayout).
+template <bool PACKED, int POS, int W, int NWORDS>
+__device__ __forceinline__ uint32_t pair_of(const uint32_t (&c)[NWORDS], uint32_t r) {
+  constexpr int w = POS / 32, s = POS % 32;
+  if constexpr (PACKED) {
+    return lut32(__byte_perm(c[w], r, 0x7604u | (uint32_t)((s / 8) << 4)));
+  } else {
+    constexpr uint32_t mask = ((1u << W) - 1u) << 7;
+    uint32_t x;
+    if constexpr (s + W > 32) x = __funnelshift_r(c[w], c[w + 1], s - 7);
+    else if constexpr (s > 7) x = c[w] >> (s - 7);
+    else x = c[w] << (7 - s);
+    return lut32((x & mask) | r);
+  }
+}
+
+// Value codes of one token for lane group gq: 16 codes of VB bits (bits past them are never used).
+template <int VB, int OFF>
+__device__ __forceinline__ void v_codes_at(uint32_t p, uint32_t odd, uint32_t (&c)[(VB + 1) / 2]) {
+  if constexpr (VB == 4) {
+    const uint2 v = ld64<OFF>(p);
+    c[0] = v.x;
+    c[1] = v.y;
+  } else if constexpr (VB == 3) {  // six bytes from byte 6 gq: p is that rounded down to a word
+    const uint32_t v0 = ld32<OFF>(p), v1 = ld32<OFF + 4>(p);
+    c[0] = __funnelshift_r(v0, v1, odd);
+    c[1] = v1 >> odd;
+  } else {
+    c[0] = ld32<OFF>(p);
+  }
+}
+// Codes of two tokens a and b field by field: even fields to e, odd fields to o, each a | b << VB.
+template <int VB, int NWORDS>
+__device__ __forceinline__ void interleave(const uint32_t (&a)[NWORDS], const uint32_t (&b)[NWORDS], uint32_t (&e)[NWORDS], uint32_t (&o)[NWORDS]) {
+  auto sel = [](uint32_t m, uint32_t x, uint32_t y) { return (x & m) | (y & ~m); };
+  if constexpr (VB == 3) {  // 3-bit fields cross the word: 6-bit period, bits 32 .. 47 in the second word
+    constexpr uint64_t m = 0x71C71C71C71C71C7ull;
+    e[0] = sel((uint32_t)m, a[0], b[0] << 3);
+    e[1] = sel((uint32_t)(m >> 32), a[1], __funnelshift_l(b[0], b[1], 3));
+    o[0] = sel((uint32_t)m, __funnelshift_r(a[0], a[1], 3), b[0]);
+    o[1] = sel((uint32_t)(m >> 32), a[1] >> 3, b[1]);
+  } else {
+    constexpr uint32_t m = VB == 4 ? 0x0F0F0F0Fu : 0x33333333u;
+#pragma unroll
+    for (int i = 0; i < NWORDS; ++i) {
+      e[i] = sel(m, a[i], b[i] << VB);
+      o[i] = sel(m, a[i] >> VB, b[i]);
     }
   }
 }
-template <int NW>
-__device__ __forceinline__ void pconsumers_sync() {
-  asm volatile("bar.sync 1, %0;\n" ::"n"(NW * 32) : "memory");
-}
+
+// Where a warp stands in the work: group gi of unit uu of sequence b, and what follows of its length.
+struct Cursor {
+  int b, uu, gi, G, first, len;
+};
 
 template <int KB, int VB, bool QJL, int NB>
-__global__ void __launch_bounds__(PShape<NB>::THREADS, 1) paged_split(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_split(const __grid_constant__ PagedArgs a) {
   using Lay = PLayout<KB, VB, QJL, NB>;
-  using Lut = PairLut<KB, VB>;
-  constexpr int NW = Lay::NW, HGN = Lay::HGN;
+  constexpr int NW = Lay::NW, HGN = Lay::HGN, DEPTH = Lay::DEPTH, SLOT = Lay::SLOT;
   extern __shared__ __align__(1024) unsigned char smem[];
-  PCtrl& ctl = *reinterpret_cast<PCtrl*>(smem + a.dyn_smem - P_CTRL_BYTES);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  if (tid == 0) {
-    place_smem<KB, VB, QJL, NB>(smem_u32(smem), a.dyn_smem, ctl);
-    ctl.err = ctl.ns ? 0u : 2u;
-    for (int i = 0; i < ctl.ns; ++i) {
-      mbar_init_(&ctl.full[i], 1);
-      mbar_init_(&ctl.empty[i], NW);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init_(&ctl.sfull[i], 1);
-      mbar_init_(&ctl.sempty[i], NW);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
+  const int U = a.Hkv * a.hgroups;  // units of a sequence
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  __syncthreads();
-  const int ns = ctl.ns;
-  if (ns == 0) {
+
+  // ---- shared memory: [front rings] tables [back rings] ... misc at the end
+  const uint32_t base = smem_u32(smem);
+  const uint32_t tbl = (base + Lay::TBL_ALIGN - 1) & ~(uint32_t)(Lay::TBL_ALIGN - 1);
+  const int front = (int)(tbl - base) / (DEPTH * SLOT);  // rings before the tables
+  const uint32_t ring = warp < front ? base + warp * (DEPTH * SLOT) : tbl + Lay::TBL_BYTES + (warp - front) * (DEPTH * SLOT);
+  unsigned char* misc = smem + P_SMEM - P_MISC;
+  int64_t* pre = reinterpret_cast<int64_t*>(misc);               // [P_LENS + 1] groups before a sequence
+  int32_t* lens = reinterpret_cast<int32_t*>(misc + 8 * P_LENS + 16);  // [P_LENS]
+  float* cbs = reinterpret_cast<float*>(misc + 12 * P_LENS + 32);     // [32]
+  int64_t* joint_rec = reinterpret_cast<int64_t*>(misc + 12 * P_LENS + 160);
+  static_assert(12 * P_LENS + 168 <= P_MISC, "misc");
+  const bool few = a.B <= P_LENS;
+  if (few)
+    for (int b = tid; b < a.B; b += Lay::THREADS) lens[b] = a.lens[b];
+  if (tid < 16) cbs[tid] = tid < (1 << KB) ? a.kc[tid] : 0.0f;
+  else if (tid < 32) cbs[tid] = tid - 16 < (1 << VB) ? a.vc[tid - 16] : 0.0f;
+  if (base + P_SMEM < tbl + Lay::TBL_BYTES + (uint32_t)(NW > front ? NW - front : 0) * (DEPTH * SLOT) + P_MISC) {
+    // dynamic shared memory starts where the rings do not fit (never on sm_100)
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (tid == 0) atomicOr(a.err, 2u);
     return;
   }
+  __syncthreads();
 
-  if (warp == NW) {
-    // ================================================================ producer
-    const int U = a.Hkv * a.hgroups;  // units of a sequence
-    // groups of sequence b, and the tokens shown
-    auto shown = [&](int b, int& first, int& len) -> int {
-      return seq_groups(a.lens[b], a.max_tokens, a.window, first, len);
-    };
-    int64_t mine = 0;
-    bool bad = false;
-#pragma unroll 8
-    for (int b = lane; b < a.B; b += 32) {
-      int first, len;
-      mine += shown(b, first, len);
-      bad = bad || a.lens[b] < 0 || a.lens[b] > a.max_tokens;
-    }
+  bool bad = false;  // a page number out of range (the prep kernel checks the lengths)
+  auto len_of = [&](int b) { return few ? lens[b] : a.lens[b]; };
+  if (few && warp == 0) {  // running sums
+    int64_t sum = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int first, len, n = b0 + lane < a.B ? lens[b0 + lane] : 0;
+      const int G = seq_groups(n, a.max_tokens, a.window, first, len);
+      int64_t x = G;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(FULL, mine, o);
-    if (__any_sync(FULL, bad) && lane == 0) atomicOr(&ctl.err, 16u);
-    const int64_t N = mine * U;
-    const int C = active_ctas(N, gridDim.x);
-    int64_t f = range_start(N, C, blockIdx.x);
-    const int64_t f_end = (int)blockIdx.x < C ? range_start(N, C, blockIdx.x + 1) : f;
-    // the sequence that holds group f: lane i keeps the groups of sequence b0 + i
-    int b0 = 0, b = 0, G = 0, first = 0, len = 0, uu = 0, gi = 0;
-    int lg = 0, lfirst = 0, llen = 0;  // this lane's sequence of the current 32
-    auto load32 = [&](int base) {
-      b0 = base;
-      lg = 0;
-      if (base + lane < a.B) lg = shown(base + lane, lfirst, llen);
-    };
-    auto pick = [&](int bb) {
-      b = bb;
-      G = __shfl_sync(FULL, lg, bb - b0);
-      first = __shfl_sync(FULL, lfirst, bb - b0);
-      len = __shfl_sync(FULL, llen, bb - b0);
-    };
-    if (f < f_end) {
-      const int64_t t = f / U;
-      int64_t before = 0;
-      for (int base = 0; base < a.B; base += 32) {
-        load32(base);
-        int64_t incl = lg;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t y = __shfl_up_sync(FULL, incl, o);
-          if (lane >= o) incl += y;
-        }
-        const unsigned m = __ballot_sync(FULL, before + incl > t);
-        if (m) {
-          const int l = __ffs(m) - 1;
-          pick(base + l);
-          before += __shfl_sync(FULL, incl, l) - G;
-          break;
-        }
-        before += __shfl_sync(FULL, incl, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
       }
-      const int64_t rem = f - before * U;
-      uu = (int)(rem / G);
-      gi = (int)(rem - (int64_t)uu * G);
+      if (b0 + lane < a.B) pre[b0 + lane] = sum + x - G;
+      sum += __shfl_sync(FULL, x, 31);
     }
-    int it = 0, issued = 0, slot = 0, round = 0, si = 0;
-    bool prep_done = false;
-    while (true) {
-      const bool done = f >= f_end;
-      const int n = done ? 0 : (int)min((int64_t)(G - gi), f_end - f);
-      const int64_t unit = (int64_t)b * U + uu;
-      // ---- the segment's stages.  Its operands come from the prep kernel, so with the first segment
-      // the ring fills before the wait for that kernel.
-      const int64_t rowh = (int64_t)(uu / a.hgroups) * a.ps;  // kv-head's rows of a page
-      const int tok0 = 16 * (first / 16 + gi);
-      auto page_of = [&](int s0) -> int {  // page of this lane's group of stage s0 (-1: none)
-        if (lane >= NW || s0 + lane >= n) return -1;
-        return a.table[(int64_t)b * a.table_stride + (tok0 + 16 * (s0 + lane)) / a.ps];
-      };
-      auto open_segment = [&]() {
-        if (!prep_done) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-        prep_done = true;
-        const int k = si & 1;
-        if (si >= 2 && !pwait(ctl, &ctl.sempty[k], ((si >> 1) - 1) & 1)) return;
-        if (lane == 0) {
-          ctl.seg[k].n = n;
-          ctl.seg[k].tok0 = tok0;
-          ctl.seg[k].first = first;
-          ctl.seg[k].len = len;
-          ctl.seg[k].slot = gi == 0 ? unit : (int64_t)a.B * U + blockIdx.x;
-          if (done) mbar_arrive_(&ctl.sfull[k]);
-          else {
-            mbar_expect_tx_(&ctl.sfull[k], Lay::SEG_BYTES);
-            bulk_g2s(smem + ctl.seg_off + k * Lay::SEG_BYTES, a.ops + unit * (Lay::SEG_BYTES / 4), Lay::SEG_BYTES, &ctl.sfull[k]);
-          }
-        }
-        __syncwarp();
-      };
-      if (done) {
-        open_segment();
-        break;
+    if (lane == 0) pre[a.B] = sum;
+  }
+  // ---- pair tables: entry e = lo | hi << b -> half2(c[lo], c[hi]), a replica per lane, four to a store
+  constexpr uint32_t K_AT = Lay::kPacked || KB >= VB ? 0 : Lay::V_TBL;
+  constexpr uint32_t V_AT = Lay::kPacked ? 128 : KB >= VB ? Lay::K_TBL : 0;
+  constexpr int PITCH = Lay::kPacked ? 256 : 128;
+  unsigned char* tp = smem + (tbl - base);
+  for (int i = tid; i < Lay::K_TBL / 16; i += Lay::THREADS) {
+    const int e = i >> 3;
+    const uint32_t v = pack_half2(cbs[e & ((1 << KB) - 1)], cbs[e >> KB]);
+    *reinterpret_cast<uint4*>(tp + K_AT + e * PITCH + 16 * (i & 7)) = make_uint4(v, v, v, v);
+  }
+  for (int i = tid; i < Lay::V_TBL / 16; i += Lay::THREADS) {
+    const int e = i >> 3;
+    const uint32_t v = pack_half2(cbs[16 + (e & ((1 << VB) - 1))], cbs[16 + (e >> VB)]);
+    *reinterpret_cast<uint4*>(tp + V_AT + e * PITCH + 16 * (i & 7)) = make_uint4(v, v, v, v);
+  }
+  const uint32_t rk = (tbl + K_AT) | (4u * lane), rv = (tbl + V_AT) | (4u * lane);
+  __syncthreads();
+  // a batch too large for shared memory: the prep kernel's sums
+  if (!few) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  auto before = [&](int b) { return few ? pre[b] : __ldcg(a.before + b); };
+  const int64_t N = before(a.B) * U;
+  const Cut cut = cut_of(N, a.ctas, NW);
+  const bool mine = (int)blockIdx.x < cut.ctas && warp < cut.warps;
+  const int W = blockIdx.x * cut.warps + warp;
+  const int64_t f0 = mine ? range_start(N, cut, W) : 0;
+  int left = mine ? (int)(range_start(N, cut, W + 1) - f0) : 0;  // groups to go
+
+  auto enter = [&](Cursor& c) { c.G = seq_groups(len_of(c.b), a.max_tokens, a.window, c.first, c.len); };
+  auto next_unit = [&](Cursor& c) {
+    c.gi = 0;
+    if (++c.uu < U) return;
+    c.uu = 0;
+    do {
+      if (++c.b >= a.B) {  // behind the last group: nothing is taken from here
+        c.b = a.B - 1;
+        c.G = 1;
+        return;
       }
-      bool opened = false;
-      if (prep_done) {
-        open_segment();
-        opened = true;
-      }
-      int page = page_of(0);
-      int stages = 0;
-      for (int s0 = 0; s0 < n; s0 += NW, ++it, ++stages) {
-        const int cur = slot, cur_round = round;
-        if (++slot == ns) {
-          slot = 0;
-          ++round;
-        }
-        if (!opened && stages == ns) {  // the ring is full: now the operands are needed
-          open_segment();
-          opened = true;
-        }
-        if (cur_round > 0 && !pwait(ctl, &ctl.empty[cur], (cur_round - 1) & 1)) continue;
-        if (*reinterpret_cast<volatile unsigned int*>(&ctl.err) & 3u) continue;
-        const int here = page;
-        page = page_of(s0 + NW);
-        const int cnt = min(NW, n - s0);
-        const int t = tok0 + 16 * (s0 + lane);
-        const int at = t % a.ps;
-        const unsigned lead = __ballot_sync(FULL, lane < cnt && (lane == 0 || at == 0));
-        if (lane == 0) mbar_expect_tx_(&ctl.full[cur], (uint32_t)(16 * cnt * Lay::TX_PER_TOKEN));
-        __syncwarp();
-        if ((lead >> lane) & 1u) {
-          const unsigned rest = lane < 31 ? lead >> (lane + 1) : 0u;
-          const int run = rest ? __ffs(rest) : cnt - lane;  // groups up to the next page
-          int p = here;
-          if ((unsigned)p >= (unsigned)a.pages) {  // a bad table entry: recorded, page 0 read instead
-            atomicOr(&ctl.err, 16u);
-            p = 0;
-          }
-          const int64_t row = (int64_t)p * a.Hkv * a.ps + rowh + at;
-          unsigned char* st = smem + ctl.stage_off[cur];
-          const uint32_t i = 16u * lane, rows = 16u * run;
-          bulk_g2s(st + Lay::OFF_KC + i * Lay::K_ROW, a.k_codes + row * Lay::K_ROW, rows * Lay::K_ROW, &ctl.full[cur]);
-          if constexpr (QJL) {
-            bulk_g2s(st + Lay::OFF_SG + i * 16, a.k_signs + row * 16, rows * 16, &ctl.full[cur]);
-            bulk_g2s(st + Lay::OFF_RN + i * 4, a.k_rnorm + row, rows * 4, &ctl.full[cur]);
-          }
-          bulk_g2s(st + Lay::OFF_VC + i * Lay::V_ROW, a.v_codes + row * Lay::V_ROW, rows * Lay::V_ROW, &ctl.full[cur]);
-          bulk_g2s(st + Lay::OFF_NK + i * 4, a.k_norm + row, rows * 4, &ctl.full[cur]);
-          bulk_g2s(st + Lay::OFF_NV + i * 4, a.v_norm + row, rows * 4, &ctl.full[cur]);
-        }
-        __syncwarp();
-        issued = it + 1;
-      }
-      if (!opened) open_segment();
-      ++si;
-      f += n;
-      // ---- the next unit
-      gi = 0;
-      if (++uu == U && f < f_end) {
-        uu = 0;
-        int nb = b + 1;
-        while (true) {  // (f < f_end: some later sequence has groups)
-          if (nb >= b0 + 32) load32(b0 + 32);
-          const unsigned m = __ballot_sync(FULL, lg > 0) & (nb - b0 == 0 ? FULL : ~((1u << (nb - b0)) - 1u));
-          if (m) {
-            pick(b0 + __ffs(m) - 1);
-            break;
-          }
-          nb = b0 + 32;
-          if (nb >= a.B) break;
-        }
-      }
+      enter(c);
+    } while (c.G == 0);
+  };
+  Cursor cur;
+  cur.b = cur.uu = cur.gi = 0;
+  cur.G = 1;
+  cur.first = cur.len = 0;
+  if (left > 0) {
+    int lo = 0, hi = a.B;  // before(lo) * U <= f0 < before(hi) * U
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid) * U <= f0) lo = mid;
+      else hi = mid;
     }
-    // every copy issued has landed before the CTA may exit (bounded)
-    for (int j = max(0, issued - ns); j < issued; ++j) {
-      const uint32_t addr = smem_u32(&ctl.full[j % ns]);
-      const long long t0 = clock64();
-      while (!__all_sync(FULL, mbar_try(addr, (j / ns) & 1)) && clock64() - t0 < P_WAIT_LIMIT) {
-      }
-    }
-    if (si > 0) {  // the last segment's operands (its buffer is not the one the closing message used)
-      const uint32_t addr = smem_u32(&ctl.sfull[(si - 1) & 1]);
-      const long long t0 = clock64();
-      while (!__all_sync(FULL, mbar_try(addr, ((si - 1) >> 1) & 1)) && clock64() - t0 < P_WAIT_LIMIT) {
-      }
-    }
-    return;
+    cur.b = lo;
+    enter(cur);
+    const int64_t rem = f0 - before(lo) * U;
+    cur.uu = (int)div64(rem, cur.G);
+    cur.gi = (int)(rem - (int64_t)cur.uu * cur.G);
   }
 
-  // ================================================================ consumers
-  // pair tables: entry e = lo | hi << b -> half2(c[lo], c[hi]), four lane replicas per 16-byte store
-  Lut lut;
-  {
-    float* cbs = reinterpret_cast<float*>(smem + ctl.merge_off);
-    if (tid < 16) cbs[tid] = tid < (1 << KB) ? a.kc[tid] : 0.0f;
-    else if (tid < 32) cbs[tid] = tid - 16 < (1 << VB) ? a.vc[tid - 16] : 0.0f;
-    pconsumers_sync<NW>();
-    const uint32_t tbl = ctl.tbl_addr;
-    unsigned char* tp = smem + (tbl - smem_u32(smem));
-    if constexpr (Lut::kPacked) {
-      for (int i = tid; i < 256 * 2 * 8; i += NW * 32) {  // (entry, half, group of four lanes)
-        const int e = i >> 4, half = (i >> 3) & 1, q4 = i & 7;
-        const float* cb = cbs + 16 * half;
-        const uint32_t v = pack_half2(cb[e & 15], cb[e >> 4]);
-        *reinterpret_cast<uint4*>(tp + e * 256 + half * 128 + 16 * q4) = make_uint4(v, v, v, v);
+  // ---- fetching.  A run is the groups of one page (of one unit): its addresses are formed once, and
+  // the page of the run after it is looked up then.
+  const int gpp = a.ps / kGroup;  // groups of a page
+  auto page_index = [&](int grp) -> int { return gpp == 1 ? grp : (int)__umul64hi((uint64_t)(uint32_t)grp, a.gpp_inv); };
+  Cursor nxt = cur;  // the next run's first group
+  int to_fetch = left, run = 0;
+  auto look_up = [&]() -> int { return __ldg(a.table + (int64_t)nxt.b * a.table_stride + page_index(nxt.first / kGroup + nxt.gi)); };
+  int page = to_fetch > 0 ? look_up() : 0;
+  // per lane: its 16 bytes of the key and value codes, and of the small arrays: lanes 0 .. 15 the signs,
+  // 16 .. 27 the norms (four lanes each)
+  const uint8_t *kc = nullptr, *vc = nullptr, *sm = nullptr;
+  const uint8_t* sm0 = lane < 16 ? (QJL ? a.k_signs : nullptr) : lane < 20 ? reinterpret_cast<const uint8_t*>(a.k_norm)
+                       : lane < 24 ? reinterpret_cast<const uint8_t*>(a.v_norm)
+                       : lane < 28 && QJL ? reinterpret_cast<const uint8_t*>(a.k_rnorm) : nullptr;
+  const int sm_row = lane < 16 ? 16 : 4;
+  const uint32_t sm_at = lane < 16 ? Lay::OFF_SG + 16 * lane : lane < 20 ? Lay::OFF_NK + 16 * (lane - 16)
+                         : lane < 24 ? Lay::OFF_NV + 16 * (lane - 20) : Lay::OFF_RN + 16 * (lane - 24);
+  if (sm0) sm0 += 16 * (lane < 16 ? lane : (lane & 3));
+  uint32_t fdst = ring;
+  auto fetch = [&]() {  // (commits a group of copies every time, empty when nothing is left)
+    if (to_fetch > 0) {
+      if (run == 0) {
+        int p = page;
+        if ((unsigned)p >= (unsigned)a.pages) {  // a bad table entry: recorded, page 0 read instead
+          bad = true;
+          p = 0;
+        }
+        const int grp = nxt.first / kGroup + nxt.gi, in_page = grp - gpp * page_index(grp);
+        const int kvh = a.hgroups == 1 ? nxt.uu : nxt.uu / a.hgroups;
+        const int64_t row = ((int64_t)p * a.Hkv + kvh) * a.ps + kGroup * in_page;
+        kc = a.k_codes + row * Lay::K_ROW + 16 * lane;
+        vc = a.v_codes + row * Lay::V_ROW + 16 * lane;
+        sm = sm0 + row * sm_row;
+        run = min(gpp - in_page, nxt.G - nxt.gi);
+        if (run < to_fetch) {
+          nxt.gi += run;
+          if (nxt.gi == nxt.G) next_unit(nxt);
+          page = look_up();
+        }
       }
-      lut.rk = tbl | (4u * lane);
-      lut.rv = tbl | 128u | (4u * lane);
-    } else {
-      for (int i = tid; i < (Lay::K_TBL + Lay::V_TBL) / 16; i += NW * 32) {
-        const bool isv = i >= Lay::K_TBL / 16;
-        const int e = (isv ? i - Lay::K_TBL / 16 : i) >> 3;
-        const int bits = isv ? VB : KB;
-        const float* cb = cbs + (isv ? 16 : 0);
-        const uint32_t v = pack_half2(cb[e & ((1 << bits) - 1)], cb[e >> bits]);
-        *reinterpret_cast<uint4*>(tp + 16 * i) = make_uint4(v, v, v, v);
-      }
-      lut.rk = tbl + 4u * lane;
-      lut.rv = tbl + Lay::K_TBL + 4u * lane;
+      const uint32_t dst = fdst + 16 * lane;
+      cp_async16_at<Lay::OFF_KC>(dst, kc);
+      if (KB == 4 || (KB == 3 && lane < 16)) cp_async16_at<Lay::OFF_KC + 512>(dst, kc + 512);
+      cp_async16_at<Lay::OFF_VC>(dst, vc);
+      if (VB == 4 || (VB == 3 && lane < 16)) cp_async16_at<Lay::OFF_VC + 512>(dst, vc + 512);
+      if (sm0) cp_async16_at<0>(fdst + sm_at, sm);
+      kc += 16 * Lay::K_ROW;
+      vc += 16 * Lay::V_ROW;
+      sm += 16 * sm_row;
+      --run;
+      --to_fetch;
+      fdst += SLOT;
+      if (fdst == ring + DEPTH * SLOT) fdst = ring;
     }
-    pconsumers_sync<NW>();
-  }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) fetch();
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
+  // Column 2t + x of a lane's sums (x = 0, 1): NB = 1: hi and lo of head t; NB = 2: heads 2t and 2t + 1.
+  constexpr int H = NB;  // heads of a lane
   const int gq = lane >> 2, t = lane & 3;
-  int slot = 0;
-  uint32_t phase = 0;
-  for (int si = 0;; ++si) {
-    const int k = si & 1;
-    if (!pwait(ctl, &ctl.sfull[k], (si >> 1) & 1)) break;
-    const int n = ctl.seg[k].n;
-    if (n == 0) break;
-    const int tok0 = ctl.seg[k].tok0, first = ctl.seg[k].first, len = ctl.seg[k].len;
-    const int64_t pslot = ctl.seg[k].slot;
+  // rows of a pair of tokens are read in swapped order by lanes with odd t (two bank groups instead of
+  // one); the weights of those lanes are swapped alike
+  const int sw = VB == 4 ? t & 1 : 0;
+  const uint32_t swap_sel = sw ? 0x1032u : 0x3210u;
+  // this lane's places in a group
+  const uint32_t k_at = Lay::OFF_KC + gq * Lay::K_ROW + 4 * KB * t;
+  const uint32_t v_at = Lay::OFF_VC + (2 * t + sw) * Lay::V_ROW + ((2 * VB * gq) & ~3);
+  const uint32_t v_odd = VB == 3 ? 16 * (gq & 1) : 0;
+  const uint32_t s_at = Lay::OFF_SG + 16 * gq + 4 * t, n_at = Lay::OFF_NK + 4 * gq;
+  // a CTA whose range lies in one unit joins its warps at the end (the merge kernel counts likewise);
+  // warp 0, which stands at the range's first group, decides
+  if (tid == 0) {
+    const int64_t begin = f0 - cur.gi;  // the unit's first group in the order of all
+    const bool j = left > 0 && range_start(N, cut, (blockIdx.x + 1) * cut.warps) <= begin + cur.G;
+    *joint_rec = !j ? -1 : cur.gi == 0 ? (int64_t)cur.b * U + cur.uu : (int64_t)a.B * U + W;
+  }
+  __syncthreads();
+  const int64_t rec_joint = *joint_rec;
+  const bool joint = rec_joint >= 0;
+  uint32_t src = ring;  // the slot in turn
+  // Sums of the values: dim block db: dims 16db + gq (columns 2t, 2t + 1 in [0], [1]) and 16db + 8 + gq
+  // ([2], [3]).
+  float oacc[8][4];
+  float m_run[H], l_run[H];
+  while (left > 0) {
+    const int64_t unit = (int64_t)cur.b * U + cur.uu;
+    const bool opens = cur.gi == 0;
+    int n = min(left, cur.G - cur.gi);
+    left -= n;
+    // B fragments of q' and S q': NB = 1: one block, hi and lo in neighbouring columns; NB = 2: block 0
+    // hi, block 1 lo
     uint32_t bq[NB][8][2], bsq[NB][8][2];
-    float fK[NB], fQ[NB], Kh[NB];
+    float fK[H], fQ[H], Kh[H];
     {
-      const unsigned char* seg = smem + ctl.seg_off + k * Lay::SEG_BYTES;
-      const uint4* fp = reinterpret_cast<const uint4*>(seg) + lane;
-      const float4* hc = reinterpret_cast<const float4*>(seg + NB * 4096);
+      const uint4* fp = reinterpret_cast<const uint4*>(a.ops + unit * (seg_bytes(NB) / 4)) + lane;
+      const float4* hc = reinterpret_cast<const float4*>(a.ops + unit * (seg_bytes(NB) / 4) + NB * 1024);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-        for (int w4 = 0; w4 < 8; ++w4) {
-          const uint4 v = fp[(nb * 8 + w4) * 32];
+        for (int w4 = 0; w4 < (QJL ? 8 : 4); ++w4) {
+          const uint4 v = __ldcg(fp + (nb * 8 + w4) * 32);
           const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int word = 4 * w4 + j;
-            if (word < 16) bq[nb][word >> 1][word & 1] = wv[j];
-            else bsq[nb][(word >> 1) & 7][word & 1] = wv[j];
+            (word < 16 ? bq : bsq)[nb][(word >> 1) & 7][word & 1] = wv[j];
           }
         }
-        const float4 h = hc[4 * nb + t];
-        fK[nb] = h.x;
-        fQ[nb] = h.y;
-        Kh[nb] = h.z;
+      }
+#pragma unroll
+      for (int x = 0; x < H; ++x) {
+        const float4 h = __ldcg(hc + NB * t + x);
+        fK[x] = h.x;
+        fQ[x] = h.y;
+        Kh[x] = h.z;
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive_(&ctl.sempty[k]);
-
-    // Output accumulators: n-block nb, dim block db: (dim 16db + gq, head 4nb + t) hi/lo in [0]/[1],
-    // (dim 16db + 8 + gq) in [2]/[3].
-    float oacc[NB][8][4];
-    float m_run[NB], l_run[NB];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
+    for (int i = 0; i < 8; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) oacc[nb][i][0] = oacc[nb][i][1] = oacc[nb][i][2] = oacc[nb][i][3] = 0.0f;
-      m_run[nb] = -1e30f;  // finite: ex2(s - m) and ex2(m_old - m_new) never see inf - inf
-      l_run[nb] = 0.0f;
+    for (int x = 0; x < H; ++x) {
+      m_run[x] = -1e30f;  // finite: ex2(s - m) and ex2(m_old - m_new) never see inf - inf
+      l_run[x] = 0.0f;
     }
+    int tk = kGroup * (cur.first / kGroup + cur.gi) + gq - cur.first;  // row gq's place among the tokens shown
+    const uint32_t shown = (uint32_t)(cur.len - cur.first);
+    for (; n > 0; --n, tk += kGroup) {
+      cp_async_wait<DEPTH - 2>();  // the oldest group has landed ...
+      __syncwarp();                // ... for every lane, and every lane is done with the slot to fill
+      fetch();
+      const bool v0ok = (uint32_t)tk < shown, v1ok = (uint32_t)(tk + 8) < shown;
 
-    for (int s0 = 0; s0 < n; s0 += NW) {
-      const bool ok = pwait(ctl, &ctl.full[slot], phase);
-      if (ok && s0 + warp < n) {
-        const unsigned char* stage = smem + ctl.stage_off[slot];
-        const int r0 = 16 * warp + gq, r1 = r0 + 8;  // this lane's token rows in the stage
-        const int tk = tok0 + 16 * (s0 + warp) + gq;
-        const bool v0ok = tk >= first && tk < len, v1ok = tk + 8 >= first && tk + 8 < len;
+      // ---- scores of tokens gq and gq + 8: products with the key codes and the sign bits in turn
+      float ka[NB][4], qa[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ka[nb][e] = qa[nb][e] = 0.0f;
+      uint32_t c0[KB], c1[KB], w0 = 0, w1 = 0;
+      const uint32_t kp = src + k_at;
+      if constexpr (KB == 4) {
+        const uint4 x0 = ld128<0>(kp), x1 = ld128<8 * Lay::K_ROW>(kp);
+        c0[0] = x0.x; c0[1] = x0.y; c0[2] = x0.z; c0[3] = x0.w;
+        c1[0] = x1.x; c1[1] = x1.y; c1[2] = x1.z; c1[3] = x1.w;
+      } else if constexpr (KB == 2) {
+        const uint2 x0 = ld64<0>(kp), x1 = ld64<8 * Lay::K_ROW>(kp);
+        c0[0] = x0.x; c0[1] = x0.y;
+        c1[0] = x1.x; c1[1] = x1.y;
+      } else {
+        c0[0] = ld32<0>(kp); c0[1] = ld32<4>(kp); c0[2] = ld32<8>(kp);
+        c1[0] = ld32<8 * Lay::K_ROW>(kp); c1[1] = ld32<8 * Lay::K_ROW + 4>(kp); c1[2] = ld32<8 * Lay::K_ROW + 8>(kp);
+      }
+      if constexpr (QJL) {
+        w0 = ld32<0>(src + s_at);
+        w1 = ld32<128>(src + s_at);
+      }
+#define TQ_STEP(KK)                                                                                   \
+      {                                                                                               \
+        const uint32_t A[4] = {pair_of<Lay::kPacked, 4 * KB * (KK), 2 * KB>(c0, rk),                   \
+                               pair_of<Lay::kPacked, 4 * KB * (KK), 2 * KB>(c1, rk),                   \
+                               pair_of<Lay::kPacked, 4 * KB * (KK) + 2 * KB, 2 * KB>(c0, rk),          \
+                               pair_of<Lay::kPacked, 4 * KB * (KK) + 2 * KB, 2 * KB>(c1, rk)};         \
+        _Pragma("unroll") for (int nb = 0; nb < NB; ++nb) mma(ka[nb], A, bq[nb][KK]);                  \
+        if constexpr (QJL) {                                                                          \
+          const uint32_t Z[4] = {sgn<2 * (KK)>(w0), sgn<2 * (KK)>(w1), sgn<2 * (KK) + 1>(w0), sgn<2 * (KK) + 1>(w1)}; \
+          _Pragma("unroll") for (int nb = 0; nb < NB; ++nb) mma(qa[nb], Z, bsq[nb][KK]);               \
+        }                                                                                             \
+      }
+      TQ_STEP(0) TQ_STEP(1) TQ_STEP(2) TQ_STEP(3) TQ_STEP(4) TQ_STEP(5) TQ_STEP(6) TQ_STEP(7)
+#undef TQ_STEP
 
-        VPairs<VB> p01, p89;
-        // Value codes of rows 2t, 2t+1, 2t+8, 2t+9 of the warp's 16, paired for the value MMAs (with
-        // 4-bit values and one n-block before the score MMAs, whose latency they then fill).
-        constexpr bool EARLY_V = VB == 4 && NB == 1;
-        auto load_vpairs = [&]() {
-          const unsigned char* vbase = stage + Lay::OFF_VC + (16 * warp) * Lay::V_ROW;
-          uint64_t cv0, cv1, cv2, cv3;
-          if constexpr (VB == 4) {
-            // lanes with odd t read their odd row first: two bank groups instead of one
-            const int sw = t & 1;
-            const uint2 a0 = lds64(vbase + (2 * t + sw) * Lay::V_ROW + 8 * gq);
-            const uint2 a1 = lds64(vbase + (2 * t + 1 - sw) * Lay::V_ROW + 8 * gq);
-            const uint2 a2 = lds64(vbase + (2 * t + 8 + sw) * Lay::V_ROW + 8 * gq);
-            const uint2 a3 = lds64(vbase + (2 * t + 9 - sw) * Lay::V_ROW + 8 * gq);
-            const uint64_t x0 = (uint64_t)a0.x | ((uint64_t)a0.y << 32), x1 = (uint64_t)a1.x | ((uint64_t)a1.y << 32);
-            const uint64_t x2 = (uint64_t)a2.x | ((uint64_t)a2.y << 32), x3 = (uint64_t)a3.x | ((uint64_t)a3.y << 32);
-            cv0 = sw ? x1 : x0;
-            cv1 = sw ? x0 : x1;
-            cv2 = sw ? x3 : x2;
-            cv3 = sw ? x2 : x3;
-          } else {
-            cv0 = load_v_chunk<VB>(vbase + (2 * t) * Lay::V_ROW, gq);
-            cv1 = load_v_chunk<VB>(vbase + (2 * t + 1) * Lay::V_ROW, gq);
-            cv2 = load_v_chunk<VB>(vbase + (2 * t + 8) * Lay::V_ROW, gq);
-            cv3 = load_v_chunk<VB>(vbase + (2 * t + 9) * Lay::V_ROW, gq);
-          }
-          p01.build(cv0, cv1);
-          p89.build(cv2, cv3);
+      // ---- online softmax (log2 units) of the lane's heads over the warp's 16 tokens
+      const uint32_t np = src + n_at;
+      const float nk0 = ldf<0>(np), nk1 = ldf<32>(np);
+      float rn0 = 0.0f, rn1 = 0.0f;
+      if constexpr (QJL) {
+        rn0 = ldf<Lay::OFF_RN - Lay::OFF_NK>(np);
+        rn1 = ldf<Lay::OFF_RN - Lay::OFF_NK + 32>(np);
+      }
+      constexpr float VSC = 0.08838834764831845f * LAZY_SCALE;  // 1 / sqrt(128)
+      const float nv0 = v0ok ? ldf<64>(np) * VSC : 0.0f;
+      const float nv1 = v1ok ? ldf<96>(np) * VSC : 0.0f;
+      float sc0[H], sc1[H];  // scores of the two tokens
+      bool over = false;
+#pragma unroll
+      for (int x = 0; x < H; ++x) {
+        // a head's sum: its columns hi + lo, or its column of the blocks hi + lo
+        auto col = [&](const float (&u)[NB][4], int row) {
+          return NB == 1 ? u[0][2 * row] + u[0][2 * row + 1] : u[0][2 * row + x] + u[NB - 1][2 * row + x];
         };
-        if constexpr (EARLY_V) load_vpairs();
-
-        // ---- scores of tokens r0, r1 and heads 4nb + t; two accumulators per product
-        float kacc[NB][4], qacc[NB][4], kacc2[NB][4], qacc2[NB][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) kacc[nb][e] = qacc[nb][e] = kacc2[nb][e] = qacc2[nb][e] = 0.0f;
-        {
-          uint32_t c0[KB], c1[KB];
-          const unsigned char* k0 = stage + Lay::OFF_KC + r0 * Lay::K_ROW + 4 * KB * t;
-          const unsigned char* k1 = stage + Lay::OFF_KC + r1 * Lay::K_ROW + 4 * KB * t;
-          if constexpr (KB == 4) {
-            const uint4 x0 = lds128(k0), x1 = lds128(k1);
-            c0[0] = x0.x; c0[1] = x0.y; c0[2] = x0.z; c0[3] = x0.w;
-            c1[0] = x1.x; c1[1] = x1.y; c1[2] = x1.z; c1[3] = x1.w;
-          } else if constexpr (KB == 2) {
-            const uint2 x0 = lds64(k0), x1 = lds64(k1);
-            c0[0] = x0.x; c0[1] = x0.y;
-            c1[0] = x1.x; c1[1] = x1.y;
-          } else {
-#pragma unroll
-            for (int i = 0; i < KB; ++i) {
-              c0[i] = reinterpret_cast<const uint32_t*>(k0)[i];
-              c1[i] = reinterpret_cast<const uint32_t*>(k1)[i];
-            }
-          }
-#define TQ_KSTEP(KK)                                                                         \
-          {                                                                                  \
-            const uint32_t A[4] = {k_pair<KB, VB, 2 * (KK)>(lut, c0), k_pair<KB, VB, 2 * (KK)>(lut, c1), \
-                                   k_pair<KB, VB, 2 * (KK) + 1>(lut, c0),                    \
-                                   k_pair<KB, VB, 2 * (KK) + 1>(lut, c1)};                   \
-            _Pragma("unroll") for (int nb = 0; nb < NB; ++nb)                                \
-                mma16816((KK) & 1 ? kacc2[nb] : kacc[nb], A, bq[nb][KK][0], bq[nb][KK][1]);    \
-          }
-          TQ_KSTEP(0) TQ_KSTEP(1) TQ_KSTEP(2) TQ_KSTEP(3) TQ_KSTEP(4) TQ_KSTEP(5) TQ_KSTEP(6) TQ_KSTEP(7)
-#undef TQ_KSTEP
-        }
+        float s0v = col(ka, 0) * (nk0 * fK[x]);
+        float s1v = col(ka, 1) * (nk1 * fK[x]);
         if constexpr (QJL) {
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(stage + Lay::OFF_SG + r0 * 16 + 4 * t);
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(stage + Lay::OFF_SG + r1 * 16 + 4 * t);
-#define TQ_SSTEP(KK)                                                                         \
-          {                                                                                  \
-            const uint32_t A[4] = {sgn<2 * (KK)>(w0), sgn<2 * (KK)>(w1), sgn<2 * (KK) + 1>(w0), \
-                                   sgn<2 * (KK) + 1>(w1)};                                   \
-            _Pragma("unroll") for (int nb = 0; nb < NB; ++nb)                                \
-                mma16816((KK) & 1 ? qacc2[nb] : qacc[nb], A, bsq[nb][KK][0], bsq[nb][KK][1]);  \
-          }
-          TQ_SSTEP(0) TQ_SSTEP(1) TQ_SSTEP(2) TQ_SSTEP(3) TQ_SSTEP(4) TQ_SSTEP(5) TQ_SSTEP(6) TQ_SSTEP(7)
-#undef TQ_SSTEP
+          s0v = fmaf(col(qa, 0) + Kh[x], rn0 * fQ[x], s0v);
+          s1v = fmaf(col(qa, 1) + Kh[x], rn1 * fQ[x], s1v);
         }
-
-        // ---- online softmax (log2 units) per head 4nb + t over the warp's 16 tokens
-        const float nk0 = *reinterpret_cast<const float*>(stage + Lay::OFF_NK + 4 * r0);
-        const float nk1 = *reinterpret_cast<const float*>(stage + Lay::OFF_NK + 4 * r1);
-        float rn0 = 0.0f, rn1 = 0.0f;
-        if constexpr (QJL) {
-          rn0 = *reinterpret_cast<const float*>(stage + Lay::OFF_RN + 4 * r0);
-          rn1 = *reinterpret_cast<const float*>(stage + Lay::OFF_RN + 4 * r1);
-        }
-        constexpr float VSC = 0.08838834764831845f;  // 1 / sqrt(128)
-        const float nv0 = v0ok ? *reinterpret_cast<const float*>(stage + Lay::OFF_NV + 4 * r0) * VSC : 0.0f;
-        const float nv1 = v1ok ? *reinterpret_cast<const float*>(stage + Lay::OFF_NV + 4 * r1) * VSC : 0.0f;
-        uint32_t bp[NB][2];
+        sc0[x] = v0ok ? s0v : -INFINITY;
+        sc1[x] = v1ok ? s1v : -INFINITY;
+        over = over || fmaxf(sc0[x], sc1[x]) > m_run[x] + LAZY;
+      }
+      if (__any_sync(FULL, over)) {  // the running maximum of some head moves
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float s0v = ((kacc[nb][0] + kacc2[nb][0]) + (kacc[nb][1] + kacc2[nb][1])) * (nk0 * fK[nb]);
-          float s1v = ((kacc[nb][2] + kacc2[nb][2]) + (kacc[nb][3] + kacc2[nb][3])) * (nk1 * fK[nb]);
-          if constexpr (QJL) {
-            s0v = fmaf(((qacc[nb][0] + qacc2[nb][0]) + (qacc[nb][1] + qacc2[nb][1])) + Kh[nb], rn0 * fQ[nb], s0v);
-            s1v = fmaf(((qacc[nb][2] + qacc2[nb][2]) + (qacc[nb][3] + qacc2[nb][3])) + Kh[nb], rn1 * fQ[nb], s1v);
-          }
-          s0v = v0ok ? s0v : -INFINITY;
-          s1v = v1ok ? s1v : -INFINITY;
-          float mx = fmaxf(s0v, s1v);
+        for (int x = 0; x < H; ++x) {
+          float mx = fmaxf(sc0[x], sc1[x]);
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-          if (mx > m_run[nb]) {  // uniform over the 8 lanes of head 4nb + t
-            const float alpha = ex2(m_run[nb] - mx);
+          mx = fmaxf(mx, m_run[x]);
+          const float alpha = ex2(m_run[x] - mx);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              oacc[nb][i][0] *= alpha;
-              oacc[nb][i][1] *= alpha;
-              oacc[nb][i][2] *= alpha;
-              oacc[nb][i][3] *= alpha;
+          for (int i = 0; i < 8; ++i) {
+            oacc[i][x] *= alpha;
+            oacc[i][2 + x] *= alpha;
+            if constexpr (NB == 1) {
+              oacc[i][1] *= alpha;
+              oacc[i][3] *= alpha;
             }
-            l_run[nb] *= alpha;
-            m_run[nb] = mx;
           }
-          const float e0 = ex2(s0v - m_run[nb]);  // ex2(-inf) = 0 for rows that are not shown
-          const float e1 = ex2(s1v - m_run[nb]);
-          l_run[nb] += e0 + e1;
-          // weights as fp16 hi + lo: row token, columns (head t, hi) and (head t, lo)
-          bp[nb][0] = movmatrix_trans(hilo_half2(e0 * nv0));  // tokens 2t, 2t+1 of column gq
-          bp[nb][1] = movmatrix_trans(hilo_half2(e1 * nv1));  // tokens 2t+8, 2t+9
+          l_run[x] *= alpha;
+          m_run[x] = mx;
         }
-
-        // ---- O'^T += Vhat^T P~
-        if constexpr (!EARLY_V) load_vpairs();
-#define TQ_VSTEP(DB)                                                                          \
-        {                                                                                     \
-          const uint32_t A[4] = {v_pair<KB, VB, 2 * (DB)>(lut, p01), v_pair<KB, VB, 2 * (DB) + 1>(lut, p01), \
-                                 v_pair<KB, VB, 2 * (DB)>(lut, p89), v_pair<KB, VB, 2 * (DB) + 1>(lut, p89)}; \
-          _Pragma("unroll") for (int nb = 0; nb < NB; ++nb)                                   \
-              mma16816(oacc[nb][DB], A, bp[nb][0], bp[nb][1]);                                 \
-        }
-        TQ_VSTEP(0) TQ_VSTEP(1) TQ_VSTEP(2) TQ_VSTEP(3) TQ_VSTEP(4) TQ_VSTEP(5) TQ_VSTEP(6) TQ_VSTEP(7)
-#undef TQ_VSTEP
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_(&ctl.empty[slot]);
-      if (++slot == ns) {
-        slot = 0;
-        phase ^= 1u;
-      }
-    }
-
-    // ---- the segment's partial: the warps' (max, sum, o') joined through shared memory
-    float* mw = reinterpret_cast<float*>(smem + ctl.merge_off);  // [NW][4]
-    float* lw = mw + NW * 4;
-    float* ow = lw + NW * 4;  // [NW][4][D]
+      // weights as fp16 hi and lo, turned from (token row, columns 2t, 2t + 1) into (column gq, tokens 2t,
+      // 2t + 1 and + 8): B fragments of the value products
+      uint32_t bp[NB][2];
+      {
+        float p0[H], p1[H];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float lq = l_run[nb];
-      lq += __shfl_xor_sync(FULL, lq, 4);
-      lq += __shfl_xor_sync(FULL, lq, 8);
-      lq += __shfl_xor_sync(FULL, lq, 16);
-      pconsumers_sync<NW>();  // the area's last use has been read
-      if (gq == 0) {
-        mw[warp * 4 + t] = m_run[nb];
-        lw[warp * 4 + t] = lq;
+        for (int x = 0; x < H; ++x) {
+          const float e0 = ex2(sc0[x] - m_run[x]);  // ex2(-inf) = 0 for rows that are not shown
+          const float e1 = ex2(sc1[x] - m_run[x]);
+          l_run[x] += e0 + e1;
+          p0[x] = e0 * nv0;
+          p1[x] = e1 * nv1;
+        }
+        if constexpr (NB == 1) {
+          bp[0][0] = movmatrix_trans(hilo_half2(p0[0]));
+          bp[0][1] = movmatrix_trans(hilo_half2(p1[0]));
+        } else {
+          auto hi_lo = [](float x, float y, uint32_t& hi, uint32_t& lo) {
+            const __half2 h = __floats2half2_rn(x, y);
+            const float2 f = __half22float2(h);
+            hi = *reinterpret_cast<const uint32_t*>(&h);
+            lo = pack_half2(x - f.x, y - f.y);
+          };
+          uint32_t h0, l0, h1, l1;
+          hi_lo(p0[0], p0[H - 1], h0, l0);
+          hi_lo(p1[0], p1[H - 1], h1, l1);
+          bp[0][0] = movmatrix_trans(h0);
+          bp[0][1] = movmatrix_trans(h1);
+          bp[NB - 1][0] = movmatrix_trans(l0);
+          bp[NB - 1][1] = movmatrix_trans(l1);
+        }
+        if constexpr (VB == 4) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            bp[nb][0] = __byte_perm(bp[nb][0], 0u, swap_sel);
+            bp[nb][1] = __byte_perm(bp[nb][1], 0u, swap_sel);
+          }
+        }
       }
-      float* o = ow + (warp * 4 + t) * D;
+
+      // ---- O'^T += Vhat^T P: token pairs (2t, 2t + 1) and (2t + 8, 2t + 9)
+      constexpr int VW = (VB + 1) / 2;
+      uint32_t e01[VW], o01[VW], e89[VW], o89[VW];
+      {
+        uint32_t x[VW], y[VW];
+        const uint32_t vp = src + v_at, vq = sw ? vp - Lay::V_ROW : vp + Lay::V_ROW;
+        v_codes_at<VB, 0>(vp, v_odd, x);
+        v_codes_at<VB, 0>(vq, v_odd, y);
+        interleave<VB>(x, y, e01, o01);
+        v_codes_at<VB, 8 * Lay::V_ROW>(vp, v_odd, x);
+        v_codes_at<VB, 8 * Lay::V_ROW>(vq, v_odd, y);
+        interleave<VB>(x, y, e89, o89);
+      }
+#define TQ_STEP(DB)                                                                                   \
+      {                                                                                               \
+        const uint32_t A[4] = {pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(e01, rv),                  \
+                               pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(o01, rv),                  \
+                               pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(e89, rv),                  \
+                               pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(o89, rv)};                 \
+        _Pragma("unroll") for (int nb = 0; nb < NB; ++nb) mma(oacc[DB], A, bp[nb]);                    \
+      }
+      TQ_STEP(0) TQ_STEP(1) TQ_STEP(2) TQ_STEP(3) TQ_STEP(4) TQ_STEP(5) TQ_STEP(6) TQ_STEP(7)
+#undef TQ_STEP
+      src += SLOT;
+      if (src == ring + DEPTH * SLOT) src = ring;
+    }
+    // on to the next unit (the segment ended there, or the range did)
+    const int64_t rec = opens ? unit : (int64_t)a.B * U + W;
+    if (left > 0) next_unit(cur);
+
+    // ---- the segment's partial
+#pragma unroll
+    for (int x = 0; x < H; ++x) {
+      l_run[x] += __shfl_xor_sync(FULL, l_run[x], 4);
+      l_run[x] += __shfl_xor_sync(FULL, l_run[x], 8);
+      l_run[x] += __shfl_xor_sync(FULL, l_run[x], 16);
+    }
+    if (joint) break;  // (the range's only segment)
+#pragma unroll
+    for (int x = 0; x < H; ++x) {
+      float* dst = a.part + (rec * HGN + NB * t + x) * PART;
+      if (gq == 0) *reinterpret_cast<float2*>(dst) = make_float2(m_run[x], l_run[x]);
 #pragma unroll
       for (int db = 0; db < 8; ++db) {
-        o[16 * db + gq] = oacc[nb][db][0] + oacc[nb][db][1];
-        o[16 * db + 8 + gq] = oacc[nb][db][2] + oacc[nb][db][3];
-      }
-      pconsumers_sync<NW>();
-      for (int idx = tid; idx < 4 * D; idx += NW * 32) {
-        const int r = idx / D, dd = idx % D;
-        float M = -1e30f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, mw[w * 4 + r]);
-        float Ls = 0.0f, O = 0.0f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float fw = ex2(mw[w * 4 + r] - M);
-          Ls = fmaf(fw, lw[w * 4 + r], Ls);
-          O = fmaf(fw, ow[(w * 4 + r) * D + dd], O);
-        }
-        float* dst = a.part + (pslot * HGN + 4 * nb + r) * PART;
-        dst[4 + dd] = O;
-        if (dd == 0) {
-          dst[0] = M;
-          dst[1] = Ls;
-        }
+        const float o0 = NB == 1 ? oacc[db][0] + oacc[db][1] : oacc[db][x];
+        const float o1 = NB == 1 ? oacc[db][2] + oacc[db][3] : oacc[db][2 + x];
+        dst[4 + 16 * db + gq] = o0 * (1.0f / LAZY_SCALE);
+        dst[4 + 16 * db + 8 + gq] = o1 * (1.0f / LAZY_SCALE);
       }
     }
   }
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  if (tid == 0) {
-    const unsigned int e = *reinterpret_cast<volatile unsigned int*>(&ctl.err);
-    if (e) atomicOr(a.err, e);
+  cp_async_wait<0>();
+  if (joint) {  // CTA-uniform
+    __syncthreads();  // the rings are free
+    // a warp's (max, sum) and o' of each head, in its own ring
+    static_assert(DEPTH * SLOT >= HGN * (2 + D) * 4, "join area");
+    if (mine) {
+      float* my = reinterpret_cast<float*>(smem + (ring - base));
+#pragma unroll
+      for (int x = 0; x < H; ++x) {
+        const int i = NB * t + x;
+        if (gq == 0) {
+          my[2 * i] = m_run[x];
+          my[2 * i + 1] = l_run[x];
+        }
+        float* o = my + 2 * HGN + i * D;
+#pragma unroll
+        for (int db = 0; db < 8; ++db) {
+          o[16 * db + gq] = NB == 1 ? oacc[db][0] + oacc[db][1] : oacc[db][x];
+          o[16 * db + 8 + gq] = NB == 1 ? oacc[db][2] + oacc[db][3] : oacc[db][2 + x];
+        }
+      }
+    }
+    __syncthreads();
+    for (int idx = tid; idx < HGN * D; idx += Lay::THREADS) {
+      const int i = idx / D, dd = idx % D;
+      auto of = [&](int w) {
+        const uint32_t r = w < front ? base + w * (DEPTH * SLOT) : tbl + Lay::TBL_BYTES + (w - front) * (DEPTH * SLOT);
+        return reinterpret_cast<const float*>(smem + (r - base));
+      };
+      float M = -1e30f, Ls = 0.0f, O = 0.0f;
+      for (int w = 0; w < cut.warps; ++w) M = fmaxf(M, of(w)[2 * i]);
+      for (int w = 0; w < cut.warps; ++w) {
+        const float* v = of(w);
+        const float fw = ex2(v[2 * i] - M);
+        Ls = fmaf(fw, v[2 * i + 1], Ls);
+        O = fmaf(fw, v[2 * HGN + i * D + dd], O);
+      }
+      float* dst = a.part + (rec_joint * HGN + i) * PART;
+      dst[4 + dd] = O * (1.0f / LAZY_SCALE);
+      if (dd == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, Ls);
+    }
   }
+  if (bad) atomicOr(a.err, 16u);
 }
 
 template <int KB, int VB, bool QJL, int NB>
 tq_status launch_paged(const PagedArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(paged_split<KB, VB, QJL, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, a.dyn_smem);
+  cudaError_t e = cudaFuncSetAttribute(paged_split<KB, VB, QJL, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.ctas);
-  cfg.blockDim = dim3(PShape<NB>::THREADS);
-  cfg.dynamicSmemBytes = a.dyn_smem;
+  cfg.blockDim = dim3((PLayout<KB, VB, QJL, NB>::THREADS));
+  cfg.dynamicSmemBytes = P_SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // dependent of the prep kernel

@@ -314,7 +314,7 @@ __device__ __forceinline__ void row_chunk(const InT* xrow, const uint8_t* xt, in
 // MX: the outlier-aware mixed layout (TQ_LAYOUT_MIXED): chunks ch = 0, 1 (coordinates 0..63) are
 // the outlier half with KB / VB bits, chunks 2, 3 the other half with one bit fewer; each half has
 // its own norm, codebook and power-of-two input scale (exact, as Pi is block-diagonal).
-template <int KB, int VB, typename InT, bool MX>
+template <int KB, int VB, typename InT, bool MX, bool PG>
 __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(smem_raw);
@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
 
     // ---- 6. coalesced stores of the tile's rows ----
     {
-      const bool paged = !MX && a.slots != nullptr;
+      constexpr bool paged = PG;  // (an instantiation of its own)
       auto prow = [&](int i) { return slot_row(a.slots[t0 + i], h, a.Hkv, a.pages, a.T_cap); };
       if constexpr (MX) {  // rows of 56 bytes: 8-byte units (any row is 8-byte aligned)
         const uint2* srk = reinterpret_cast<const uint2*>(s.kst);
@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
       } else {
         const uint4* srk = reinterpret_cast<const uint4*>(s.kst);
         uint4* dsk = reinterpret_cast<uint4*>(a.k_codes + row0 * K_ROW);
-        if (paged) {
+        if constexpr (paged) {
           for (int i = tid; i < nt * KB; i += THREADS)
             if (prow(i / KB) >= 0) reinterpret_cast<uint4*>(a.k_codes)[prow(i / KB) * KB + i % KB] = srk[i];
         } else {
@@ -911,7 +911,7 @@ __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
         }
         const uint4* srv = reinterpret_cast<const uint4*>(s.vst);
         uint4* dsv = reinterpret_cast<uint4*>(a.v_codes + row0 * V_ROW);
-        if (paged) {
+        if constexpr (paged) {
           for (int i = tid; i < nt * VB; i += THREADS)
             if (prow(i / VB) >= 0) reinterpret_cast<uint4*>(a.v_codes)[prow(i / VB) * VB + i % VB] = srv[i];
         } else {
@@ -923,12 +923,12 @@ __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
         src = reinterpret_cast<const uint4*>(s.sst);
         for (int i = tid; i < nt; i += THREADS) {
           const int64_t to = paged ? prow(i) : row0 + i;
-          if (to >= 0) reinterpret_cast<uint4*>(a.k_signs)[to] = src[i];
+          if (!paged || to >= 0) reinterpret_cast<uint4*>(a.k_signs)[to] = src[i];
         }
       }
       for (int i = tid; i < nt; i += THREADS) {
         const int64_t to = paged ? prow(i) : row0 + i;
-        if (to < 0) continue;
+        if (paged && to < 0) continue;
         if constexpr (MX) {
           reinterpret_cast<float2*>(a.k_norm)[to] = make_float2(s.kn[i], s.kn2[i]);
           reinterpret_cast<float2*>(a.v_norm)[to] = make_float2(s.vn[i], s.vn2[i]);
@@ -948,15 +948,15 @@ __global__ void __launch_bounds__(THREADS, 1) quantize_kernel(QArgs a) {
   if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-template <int KB, int VB, typename InT, bool MX = false>
+template <int KB, int VB, typename InT, bool MX = false, bool PG = false>
 tq_status launch3(const QArgs& a, int sms, cudaStream_t stream) {
   const size_t smem = sizeof(Smem);
-  cudaError_t e = cudaFuncSetAttribute(quantize_kernel<KB, VB, InT, MX>,
+  cudaError_t e = cudaFuncSetAttribute(quantize_kernel<KB, VB, InT, MX, PG>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
   const int64_t total = (int64_t)a.B * a.Hkv * ((a.T_new + TM - 1) / TM);
   const int grid = (int)(total < sms ? total : sms);
-  quantize_kernel<KB, VB, InT, MX><<<grid, THREADS, smem, stream>>>(a);
+  quantize_kernel<KB, VB, InT, MX, PG><<<grid, THREADS, smem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "quantize launch: %s", cudaGetErrorString(e));
   return TQ_OK;
@@ -990,13 +990,13 @@ void fill_args(QArgs& a, const tq_params* params, const tq_cache* cache, int dty
   a.guard = dtype == TQ_F32 ? Guards{4e-6f, 4e-3f, 3e-5f} : Guards{4e-6f, 4e-6f, 3e-5f};
 }
 
-template <typename InT>
+template <typename InT, bool PG = false>
 tq_status launch(int kb, int vb, const QArgs& a, int sms, cudaStream_t s) {
 #define TQ_V(KB)                                        \
   switch (vb) {                                         \
-    case 2: return launch3<KB, 2, InT>(a, sms, s);      \
-    case 3: return launch3<KB, 3, InT>(a, sms, s);      \
-    default: return launch3<KB, 4, InT>(a, sms, s);     \
+    case 2: return launch3<KB, 2, InT, false, PG>(a, sms, s); \
+    case 3: return launch3<KB, 3, InT, false, PG>(a, sms, s); \
+    default: return launch3<KB, 4, InT, false, PG>(a, sms, s); \
   }
   switch (kb) {
     case 2: TQ_V(2)
@@ -1039,8 +1039,8 @@ tq_status quantize_general_paged(const tq_params* p, const void* k, const void* 
   a.B = 1;  // of the inputs
   a.slots = slots;
   a.pages = c->B;
-  return dtype == TQ_F32 ? launch<float>(c->k_bits, c->v_bits, a, sms, stream)
-                         : launch<__nv_bfloat16>(c->k_bits, c->v_bits, a, sms, stream);
+  return dtype == TQ_F32 ? launch<float, true>(c->k_bits, c->v_bits, a, sms, stream)
+                         : launch<__nv_bfloat16, true>(c->k_bits, c->v_bits, a, sms, stream);
 }
 }  // namespace tq
 

@@ -174,9 +174,11 @@ struct __align__(1024) PSmem {
 
 static_assert(sizeof(PSmem) <= 232448, "shared memory per CTA");
 
-// Cache row of token t of (b, h); -1: a paged token that has no place (padding).
+// Cache row of token t of (b, h); -1: a paged token that has no place (padding).  PG: the cache is a
+// paged pool (an instantiation of its own, so that the contiguous kernel carries none of it).
+template <bool PG>
 __device__ __forceinline__ int64_t cache_row(const PArgs& a, int b, int h, int t) {
-  if (a.slots) return slot_row(a.slots[t], h, a.Hkv, a.pages, a.T_cap);
+  if constexpr (PG) return slot_row(a.slots[t], h, a.Hkv, a.pages, a.T_cap);
   return ((int64_t)b * a.Hkv + h) * a.T_cap + a.t_offset + t;
 }
 
@@ -600,7 +602,7 @@ __device__ __forceinline__ void set_code(uint8_t* row, int bits, int slot, uint3
   }
 }
 
-template <int KB, int VB>
+template <int KB, int VB, bool PG>
 __device__ __forceinline__ void fix_entry(PSmem& s, const PArgs& a, const FixEntry& E, int w) {
   const int lane = threadIdx.x & 31;
   constexpr int LK = 1 << KB, LV = 1 << VB;
@@ -608,8 +610,8 @@ __device__ __forceinline__ void fix_entry(PSmem& s, const PArgs& a, const FixEnt
   const int t = (int)(E.tile % (uint32_t)a.tiles_per_bh) * TM + E.r;
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   const int64_t in_off = (int64_t)b * a.sb + (int64_t)h * a.sh + (int64_t)t * a.st;
-  const int64_t row = cache_row(a, b, h, t);
-  if (row < 0) return;
+  const int64_t row = cache_row<PG>(a, b, h, t);
+  if (PG && row < 0) return;
   const double sqd = sqrt((double)D);
   unsigned int ncodes = 0, nexempt = 0;
   if (E.flags & 2) {
@@ -946,7 +948,7 @@ __device__ __forceinline__ void scatter_rows(const uint8_t* st, int pitch, uint8
 // Iteration it converts tile it (one row per thread, in place to fp16; norms and row info), then
 // finishes tile it-1: sign bits of S rho (thread = TMEM lane = row, all 128 sketch rows), and,
 // once the epilogue has staged the codes, the copy of the tile to global memory.
-template <int KB, int VB>
+template <int KB, int VB, bool PG>
 __device__ __noinline__ void role_conv(const PArgs& a, uint32_t tmem, int n_tiles) {
   PSmem& s = smem();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1035,8 +1037,8 @@ __device__ __noinline__ void role_conv(const PArgs& a, uint32_t tmem, int n_tile
     // ---- the epilogue has staged the codes of tile ut: copy the tile out ----
     if (!pwait_w(s, &s.fw, ut & 1)) break;
     if (ut == 0) wait_prior_grid();
-    const int64_t prow = a.slots && r < nt ? cache_row(a, b, h, t0 + r) : -1;
-    if (r < nt && (smk[0] | smk[1] | smk[2] | smk[3]) && (!a.slots || prow >= 0)) {
+    const int64_t prow = PG && r < nt ? cache_row<PG>(a, b, h, t0 + r) : -1;
+    if (r < nt && (smk[0] | smk[1] | smk[2] | smk[3]) && (!PG || prow >= 0)) {
       FixEntry E;
       E.tile = (uint32_t)tile;
       E.r = (uint16_t)r;
@@ -1049,7 +1051,7 @@ __device__ __noinline__ void role_conv(const PArgs& a, uint32_t tmem, int n_tile
       E.seqt = (uint32_t)ut;
       push_fix(s, a, E);
     }
-    if (a.slots) {
+    if constexpr (PG) {
       scatter_rows<KB>(s.kst, 16 * KB + 4, a.k_codes, 32 * warp, prow);
       scatter_rows<VB>(s.vst, 16 * VB + 4, a.v_codes, 32 * warp, prow);
       if (qjl) scatter_rows<1>(s.sst, 16, a.k_signs, 32 * warp, prow);
@@ -1058,8 +1060,8 @@ __device__ __noinline__ void role_conv(const PArgs& a, uint32_t tmem, int n_tile
       copy_rows<VB>(s.vst, 16 * VB + 4, a.v_codes + row0 * (16 * VB), nt, tid);
       if (qjl) copy_rows<1>(s.sst, 16, a.k_signs + row0 * 16, nt, tid);
     }
-    const int64_t rown = a.slots ? prow : row0 + r;
-    if (r < nt && rown >= 0) {
+    const int64_t rown = PG ? prow : row0 + r;
+    if (r < nt && (!PG || prow >= 0)) {
       const float nk = s.nrk[bb][r];
       a.k_norm[rown] = nk;
       a.v_norm[rown] = s.nrv[bb][r];
@@ -1227,7 +1229,7 @@ __device__ __noinline__ void role_epi(const PArgs& a, uint32_t tmem, int n_tiles
 }
 
 // ================================================================ fp64 fixups (warps 14-15)
-template <int KB, int VB>
+template <int KB, int VB, bool PG>
 __device__ __noinline__ void role_fix(const PArgs& a) {
   PSmem& s = smem();
   wait_prior_grid();
@@ -1242,7 +1244,7 @@ __device__ __noinline__ void role_fix(const PArgs& a) {
       __threadfence_block();
       const FixEntry E = *src;
       if (E.seqt < stored) {  // its tile is in global memory: patch it
-        fix_entry<KB, VB>(s, a, E, w);
+        fix_entry<KB, VB, PG>(s, a, E, w);
         k += N_FIX;
         ++done_count;
         __syncwarp();
@@ -1272,7 +1274,7 @@ __device__ __noinline__ void role_fix(const PArgs& a) {
 // finished (the rows are in global memory; no other fixup touches them any more).  Per row: the
 // exact norm; u_j = sqrt(128) (Pi x)_j / ||x|| by four threads per coordinate, then its code and
 // rho_j; (S rho)_l by four threads per sketch row; then the row's codes, signs and ||r||.
-template <int KB, int VB>
+template <int KB, int VB, bool PG>
 __device__ __noinline__ void coop_slow_rows(const PArgs& a) {
   PSmem& s = smem();
   constexpr int LK = 1 << KB;
@@ -1290,7 +1292,7 @@ __device__ __noinline__ void coop_slow_rows(const PArgs& a) {
     const int t = (int)(tile % (uint32_t)a.tiles_per_bh) * TM + r;
     const int b = bh / a.Hkv, h = bh % a.Hkv;
     const int64_t in_off = (int64_t)b * a.sb + (int64_t)h * a.sh + (int64_t)t * a.st;
-    const int64_t row = cache_row(a, b, h, t);  // (a row without a place was never queued)
+    const int64_t row = cache_row<PG>(a, b, h, t);  // (a row without a place was never queued)
     // 1. the input row in fp64 and ||x||^2 (warps 0 and 1)
     if (tid < 64) {
       const uint32_t w2 = reinterpret_cast<const uint32_t*>(a.k + in_off)[tid];
@@ -1374,7 +1376,7 @@ __device__ __noinline__ void coop_slow_rows(const PArgs& a) {
   }
 }
 
-template <int KB, int VB>
+template <int KB, int VB, bool PG>
 __global__ void __launch_bounds__(THREADS, 1)
     quantize_pipe_kernel(const __grid_constant__ PArgs a, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv) {
@@ -1460,16 +1462,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == W_TMA) role_tma(a, &tmk, &tmv, n_tiles, pre);
   else if (warp == W_MMA) role_mma(a, tmem, n_tiles);
-  else if (warp < N_CONV_WARPS) role_conv<KB, VB>(a, tmem, n_tiles);
+  else if (warp < N_CONV_WARPS) role_conv<KB, VB, PG>(a, tmem, n_tiles);
   else if (warp >= W_EPI && warp < W_EPI + N_EPI_WARPS) role_epi<KB, VB>(a, tmem, n_tiles);
-  else if (warp >= W_FIX && warp < W_FIX + N_FIX) role_fix<KB, VB>(a);
+  else if (warp >= W_FIX && warp < W_FIX + N_FIX) role_fix<KB, VB, PG>(a);
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (s.n_slow && !s.err) {
     wait_prior_grid();
-    coop_slow_rows<KB, VB>(a);
+    coop_slow_rows<KB, VB, PG>(a);
   }
   if (tid == 0 && s.err) atomicOr(&g_pipe_error, s.err);
   if (warp == W_MMA) tmem_dealloc(tmem, TMEM_COLS);
@@ -1517,10 +1519,10 @@ bool make_map(CUtensorMap* m, const void* base, int B, int Hkv, int T_new, int64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KB, int VB>
+template <int KB, int VB, bool PG>
 tq_status launch_kv(const PArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t stream) {
   const size_t smem = sizeof(PSmem);
-  cudaError_t err = cudaFuncSetAttribute(quantize_pipe_kernel<KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t err = cudaFuncSetAttribute(quantize_pipe_kernel<KB, VB, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
   if (err != cudaSuccess) return fail(TQ_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(err));
   // programmatic dependent launch: when the previous kernel of the stream is a quantize launch
@@ -1535,7 +1537,7 @@ tq_status launch_kv(const PArgs& a, const CUtensorMap& mk, const CUtensorMap& mv
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, quantize_pipe_kernel<KB, VB>, a, mk, mv);
+  err = cudaLaunchKernelEx(&cfg, quantize_pipe_kernel<KB, VB, PG>, a, mk, mv);
   if (err != cudaSuccess) return fail(TQ_ERR_CUDA, "quantize launch: %s", cudaGetErrorString(err));
   return TQ_OK;
 }
@@ -1595,9 +1597,9 @@ tq_status quantize_bf16_pipeline(const tq_params* p, const void* k, const void* 
   const int kb = c->k_bits, vb = c->v_bits;
 #define TQ_PV(KB)                                                   \
   switch (vb) {                                                     \
-    case 2: return launch_kv<KB, 2>(a, mk, mv, grid, stream);       \
-    case 3: return launch_kv<KB, 3>(a, mk, mv, grid, stream);       \
-    default: return launch_kv<KB, 4>(a, mk, mv, grid, stream);      \
+    case 2: return slots ? launch_kv<KB, 2, true>(a, mk, mv, grid, stream) : launch_kv<KB, 2, false>(a, mk, mv, grid, stream); \
+    case 3: return slots ? launch_kv<KB, 3, true>(a, mk, mv, grid, stream) : launch_kv<KB, 3, false>(a, mk, mv, grid, stream); \
+    default: return slots ? launch_kv<KB, 4, true>(a, mk, mv, grid, stream) : launch_kv<KB, 4, false>(a, mk, mv, grid, stream); \
   }
   switch (kb) {
     case 2: TQ_PV(2)

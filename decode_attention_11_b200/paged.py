@@ -31,26 +31,27 @@ _STATUS = {TQ_PAGES_NO_ROOM: "not enough free pages", TQ_PAGES_BAD_INDEX: "a num
            TQ_PAGES_SHARED: "growth inside a shared page"}
 
 
+def _elsewhere(device: torch.device, stream) -> bool:
+    """Whether the tensors' device or the call's stream is not the current one.  Such a call is made again
+    under `_on`, so that what it allocates belongs to that stream; the usual call pays for one test."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
+    if stream is None:
+        return device.index != torch.cuda.current_device()
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+    return True
+
+
 @contextlib.contextmanager
 def _on(device: torch.device, stream):
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
 
 
-def _here(device: torch.device, stream):
-    """Context in which the tensors' device and the call's stream are the current ones, so that what a
-    call allocates belongs to that stream.  Nothing to do in the usual case."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, not {device}")
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream of {stream.device}, tensors on {device}")
-    return _on(device, stream)
-
-
 def _raw_stream(device: torch.device) -> Optional[int]:
-    return torch.cuda.current_stream(device).cuda_stream or None
+    """Handle of the device's current stream (what torch.cuda.current_stream(device) wraps)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) or None
 
 
 def _int32(t: torch.Tensor, name: str, device: torch.device, dim: int = 1) -> torch.Tensor:
@@ -76,10 +77,18 @@ def _axes_of(sections: Tuple[int, ...]) -> bytes:
     return bytes(a for a, s in enumerate(sections) for _ in range(s))
 
 
-def _heads(x: torch.Tensor, name: str, N: int) -> torch.Tensor:
+def _rope_arg(x: Optional[torch.Tensor], out: Optional[torch.Tensor], name: str, N: int):
+    """((pointer, strides, heads) of x, its output)."""
+    if x is None:
+        return (None, 0, 0, 0), None
     if x.dim() != 3 or x.shape[0] != N or x.shape[2] != 128 or x.stride(2) != 1:
         raise ValueError(f"{name} must be [N, H, 128] with a contiguous last dim, N = {N}")
-    return x
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
+        raise ValueError(f"{name}_out must be contiguous, of the shape and dtype of {name}")
+    sn, sh, _ = x.stride()
+    return (x.data_ptr(), sn, sh, x.shape[1]), out
 
 
 def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor, sections: Sequence[int] = (64,),
@@ -107,23 +116,14 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor
     if q is not None and k is not None and q.dtype != k.dtype:
         raise ValueError("q and k must share their dtype")
     dt = _dtype_code(x)
-    with _here(device, stream):
-        args, outs = [], []
-        for t, o, n in ((q, q_out, "q"), (k, k_out, "k")):
-            if t is None:
-                args.append((None, 0, 0, 0))
-                outs.append(None)
-                continue
-            _heads(t, n, N)
-            if o is None:
-                o = torch.empty(t.shape, dtype=t.dtype, device=device)
-            elif o.shape != t.shape or o.dtype != t.dtype or not o.is_contiguous():
-                raise ValueError(f"{n}_out must be contiguous, of the shape and dtype of {n}")
-            args.append((t.data_ptr(), t.stride(0), t.stride(1), t.shape[1]))
-            outs.append(o)
-        _check(lib().tq_rope(*args[0], *args[1], dt, N, pos.data_ptr(), pos.stride(0), pos.shape[0], axes, float(base),
-                             int(style), int(bool(inverse)), _ptr(outs[0]), _ptr(outs[1]), _raw_stream(device)))
-    return outs[0], outs[1]
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return rope(q, k, pos, sections, base, style, inverse, axis_of_pair, q_out, k_out)
+    qa, q_out = _rope_arg(q, q_out, "q", N)
+    ka, k_out = _rope_arg(k, k_out, "k", N)
+    _check(lib().tq_rope(*qa, *ka, dt, N, pos.data_ptr(), pos.stride(0), pos.shape[0], axes, base, style, 1 if inverse else 0,
+                         _ptr(q_out), _ptr(k_out), _raw_stream(device)))
+    return q_out, k_out
 
 
 # ---------------------------------------------------------------------------------------- page table
@@ -179,11 +179,13 @@ def pages_reserve(pt: PageTable, seqs: torch.Tensor, new_tokens: torch.Tensor, n
     if seqs.shape != new_tokens.shape:
         raise ValueError("seqs and new_tokens must have the same length")
     c = pt.as_c()
-    with _here(device, stream):
-        slots = torch.empty(int(n_slots), dtype=torch.int32, device=device)
-        ws = _workspace(c, seqs.shape[0], device)
-        _check(lib().tq_pages_reserve(ctypes.byref(c), seqs.data_ptr(), new_tokens.data_ptr(), seqs.shape[0],
-                                      slots.data_ptr() or None, int(n_slots), ws.data_ptr(), ws.numel(), _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return pages_reserve(pt, seqs, new_tokens, n_slots)
+    slots = torch.empty(int(n_slots), dtype=torch.int32, device=device)
+    ws = _workspace(c, seqs.shape[0], device)
+    _check(lib().tq_pages_reserve(ctypes.byref(c), seqs.data_ptr(), new_tokens.data_ptr(), seqs.shape[0],
+                                  slots.data_ptr() or None, int(n_slots), ws.data_ptr(), ws.numel(), _raw_stream(device)))
     return slots
 
 
@@ -194,10 +196,12 @@ def pages_fork(pt: PageTable, src: torch.Tensor, dst: torch.Tensor, caches: Sequ
     if src.shape != dst.shape:
         raise ValueError("src and dst must have the same length")
     c, pools = pt.as_c(), _caches(caches, device)
-    with _here(device, stream):
-        ws = _workspace(c, src.shape[0], device)
-        _check(lib().tq_pages_fork(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), src.shape[0], pools, len(caches),
-                                   ws.data_ptr(), ws.numel(), _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return pages_fork(pt, src, dst, caches)
+    ws = _workspace(c, src.shape[0], device)
+    _check(lib().tq_pages_fork(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), src.shape[0], pools, len(caches),
+                               ws.data_ptr(), ws.numel(), _raw_stream(device)))
 
 
 def pages_free(pt: PageTable, seqs: torch.Tensor, stream=None) -> None:
@@ -205,17 +209,21 @@ def pages_free(pt: PageTable, seqs: torch.Tensor, stream=None) -> None:
     device = pt.table.device
     _int32(seqs, "seqs", device)
     c = pt.as_c()
-    with _here(device, stream):
-        _check(lib().tq_pages_free(ctypes.byref(c), seqs.data_ptr(), seqs.shape[0], _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return pages_free(pt, seqs)
+    _check(lib().tq_pages_free(ctypes.byref(c), seqs.data_ptr(), seqs.shape[0], _raw_stream(device)))
 
 
 def pages_compact(pt: PageTable, caches: Sequence[Cache], stream=None) -> None:
     """Move the pages in use to the lowest page numbers, in every pool (tq_pages_compact)."""
     device = pt.table.device
     c, pools = pt.as_c(), _caches(caches, device)
-    with _here(device, stream):
-        ws = _workspace(c, 0, device)
-        _check(lib().tq_pages_compact(ctypes.byref(c), pools, len(caches), ws.data_ptr(), ws.numel(), _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return pages_compact(pt, caches)
+    ws = _workspace(c, 0, device)
+    _check(lib().tq_pages_compact(ctypes.byref(c), pools, len(caches), ws.data_ptr(), ws.numel(), _raw_stream(device)))
 
 
 def pages_copy(caches: Sequence[Cache], src: torch.Tensor, dst: torch.Tensor, status: Optional[torch.Tensor] = None,
@@ -230,9 +238,11 @@ def pages_copy(caches: Sequence[Cache], src: torch.Tensor, dst: torch.Tensor, st
         if status.shape[0] != 1:
             raise ValueError("status must have one entry")
     pools = _caches(caches, device)
-    with _here(device, stream):
-        _check(lib().tq_pages_copy(pools, len(caches), src.data_ptr(), dst.data_ptr(), src.shape[0], _ptr(status),
-                                   _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return pages_copy(caches, src, dst, status)
+    _check(lib().tq_pages_copy(pools, len(caches), src.data_ptr(), dst.data_ptr(), src.shape[0], _ptr(status),
+                               _raw_stream(device)))
 
 
 # ---------------------------------------------------------------------------------------- rows
@@ -255,9 +265,11 @@ def paged_quantize(params: Params, k: torch.Tensor, v: torch.Tensor, pool: Cache
     _same_device(device, v, pool.k_codes, params.Pi)
     _slots(slots, k.shape[0], device)
     c, p = pool.as_c(), params.as_c()
-    with _here(device, stream):
-        _check(lib().tq_paged_quantize(ctypes.byref(p), k.data_ptr(), v.data_ptr(), _dtype_code(k), k.stride(0),
-                                       k.stride(1), k.shape[0], slots.data_ptr(), ctypes.byref(c), _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return paged_quantize(params, k, v, pool, slots)
+    _check(lib().tq_paged_quantize(ctypes.byref(p), k.data_ptr(), v.data_ptr(), _dtype_code(k), k.stride(0),
+                                   k.stride(1), k.shape[0], slots.data_ptr(), ctypes.byref(c), _raw_stream(device)))
 
 
 def paged_read(params: Params, pool: Cache, slots: torch.Tensor, dtype: torch.dtype = torch.float32, stream=None):
@@ -271,13 +283,15 @@ def paged_read(params: Params, pool: Cache, slots: torch.Tensor, dtype: torch.dt
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"unsupported dtype {dtype}")
     c, p = pool.as_c(), params.as_c()
-    with _here(device, stream):
-        k = torch.empty(N, H, 128, dtype=dtype, device=device)
-        v = torch.empty(N, H, 128, dtype=dtype, device=device)
-        signs = torch.empty(N, H, 128, dtype=torch.int8, device=device) if pool.qjl_m else None
-        rnorm = torch.empty(N, H, dtype=torch.float32, device=device) if pool.qjl_m else None
-        _check(lib().tq_paged_read(ctypes.byref(p), ctypes.byref(c), slots.data_ptr(), N, _dtype_code(k), k.data_ptr(),
-                                   v.data_ptr(), _ptr(signs), _ptr(rnorm), _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return paged_read(params, pool, slots, dtype)
+    k = torch.empty(N, H, 128, dtype=dtype, device=device)
+    v = torch.empty(N, H, 128, dtype=dtype, device=device)
+    signs = torch.empty(N, H, 128, dtype=torch.int8, device=device) if pool.qjl_m else None
+    rnorm = torch.empty(N, H, dtype=torch.float32, device=device) if pool.qjl_m else None
+    _check(lib().tq_paged_read(ctypes.byref(p), ctypes.byref(c), slots.data_ptr(), N, _dtype_code(k), k.data_ptr(),
+                               v.data_ptr(), _ptr(signs), _ptr(rnorm), _raw_stream(device)))
     return k, v, signs, rnorm
 
 
@@ -306,21 +320,23 @@ def paged_decode_attn(params: Params, q: torch.Tensor, pool: Cache, table: torch
     if seq_lens.shape[0] != B:
         raise ValueError(f"seq_lens must have {B} entries")
     c, p = pool.as_c(), params.as_c()
-    with _here(device, stream):
-        if out is None:
-            out = torch.empty(B, Hq, 128, dtype=out_dtype, device=device)
-        elif out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("out must be a contiguous [B, Hq, 128] tensor")
-        if lse is None:
-            lse = torch.empty(B, Hq, dtype=torch.float32, device=device) if return_lse else None
-        elif lse.shape != (B, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous fp32 [B, Hq] tensor")
-        if workspace is None:
-            workspace = torch.empty(max(16, lib().tq_paged_decode_workspace_size(B, Hq, ctypes.byref(c))), dtype=torch.uint8,
-                                    device=device)
-        _check(lib().tq_paged_decode_attn(
-            ctypes.byref(p), q.data_ptr(), _dtype_code(q), B, Hq, ctypes.byref(c), table.data_ptr(),
-            table.stride(0) if B > 1 else max(table.stride(0), table.shape[1]), table.shape[1], seq_lens.data_ptr(),
-            int(window), float(scale), out.data_ptr(), _dtype_code(out), _ptr(lse), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _raw_stream(device)))
+    if _elsewhere(device, stream):
+        with _on(device, stream):
+            return paged_decode_attn(params, q, pool, table, seq_lens, window, scale, out_dtype, out, return_lse, lse, workspace)
+    if out is None:
+        out = torch.empty(B, Hq, 128, dtype=out_dtype, device=device)
+    elif out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [B, Hq, 128] tensor")
+    if lse is None:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=device) if return_lse else None
+    elif lse.shape != (B, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [B, Hq] tensor")
+    if workspace is None:
+        workspace = torch.empty(max(16, lib().tq_paged_decode_workspace_size(B, Hq, ctypes.byref(c))), dtype=torch.uint8,
+                                device=device)
+    _check(lib().tq_paged_decode_attn(
+        ctypes.byref(p), q.data_ptr(), _dtype_code(q), B, Hq, ctypes.byref(c), table.data_ptr(),
+        table.stride(0) if B > 1 else max(table.stride(0), table.shape[1]), table.shape[1], seq_lens.data_ptr(),
+        int(window), float(scale), out.data_ptr(), _dtype_code(out), _ptr(lse), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(device)))
     return (out, lse) if return_lse else out
