@@ -12,10 +12,11 @@ namespace tq {
 
 constexpr int kGroup = kPageTokens;  // tokens of a group: the unit of work, inside one page
 
-// Warps of a split CTA: 16 (128 registers a thread) for up to four heads per unit (nb = 1), 12 (168) for
-// up to eight.
+// Warps of a split CTA: 12, three per scheduler with 168 registers a thread.  (Four heads per unit at 128K x 4:
+// 168 us, against 185 us with 8 or 16 warps and 190 to 215 us with 13 to 15, which load schedulers unevenly;
+// eight heads: 139 us with 8 or 12, 146 to 177 us with 4, 9, 10 or 11.)
 #ifndef PNW1
-#define PNW1 16
+#define PNW1 12
 #endif
 #ifndef PNW2
 #define PNW2 12

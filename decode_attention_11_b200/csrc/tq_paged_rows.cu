@@ -3,11 +3,13 @@
 // Quantize has two routes.  Many rows go through the tcgen05 pipeline of tq_quantize (or its general
 // kernel for fp32), which take a slot per token.  A decode step's few rows would leave that pipeline
 // with a tile or two per SM and its full depth of latency, so they have a kernel of their own here:
-// a CTA takes up to ROWS (token, kv-head) rows, holds a quarter row of Pi, then of S, per thread in
-// fp64 registers, and does the definition's arithmetic directly in fp64:
+// a CTA takes up to ROWS (token, kv-head) rows, whose keys and values are the eight columns of fp64
+// matrix products with Pi, then S (each warp keeps 16 matrix rows in registers), and does the
+// definition's arithmetic directly in fp64:
 //   n = ||x||, u = sqrt(128) Pi x / n, idx = #{t_i <= u}, rho = u - c[idx], ||r|| = n ||rho|| / sqrt(128),
 //   sign bits of S rho.
-// No guard bands and no second pass are needed.  It is bound by fp64 arithmetic: 49152 products a row.
+// No guard bands and no second pass are needed.  (Plain fp64 dot products, four threads a matrix row, took
+// 18 us for 512 rows, bound by reading the vectors from shared memory.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,48 +51,18 @@ constexpr int ROWS = 4;
 // Rows per SM up to which the fp64 kernel is used (about 0.5 us a row and SM, against the pipeline's
 // fixed cost).
 constexpr int kRowKernelPerSm = 32;
-constexpr int QT = 512;  // threads: four per coordinate
+constexpr int QT = 256;    // eight warps of 16 matrix rows
+constexpr int XS = D + 2;  // stride of a vector in shared memory (in doubles; no bank conflicts)
 
 struct RowSmem {
-  double x[2 * ROWS][D];   // keys (rows 0 .. ROWS-1), values
-  double rho[ROWS][D];
+  double x[2 * ROWS][XS];  // keys (0 .. ROWS-1), values
+  double rho[2 * ROWS][XS];
   double n[2 * ROWS];
   double r2[ROWS];
   uint32_t kw[ROWS][16], vw[ROWS][16], sw[ROWS][4];  // packed rows
   float kc[16], kt[16], vc[16], vt[16];
 };
 
-// A thread's quarter of row j of a matrix: float4 4 k + q of the row, k = 0 .. 7, in fp64.
-__device__ __forceinline__ void load_quarter(const float* M, int j, int q, double (&m)[32]) {
-  const float4* p = reinterpret_cast<const float4*>(M + j * D) + q;
-  float4 f[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = __ldg(p + 4 * k);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    m[4 * k] = (double)f[k].x;
-    m[4 * k + 1] = (double)f[k].y;
-    m[4 * k + 2] = (double)f[k].z;
-    m[4 * k + 3] = (double)f[k].w;
-  }
-}
-// The row's dot product with x (shared memory), on all four threads of the row.
-__device__ __forceinline__ double dot_quarter(const double (&m)[32], const double* x, int q) {
-  double a0 = 0.0, a1 = 0.0;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const double2* v = reinterpret_cast<const double2*>(x + 16 * k + 4 * q);
-    const double2 v0 = v[0], v1 = v[1];
-    a0 = fma(m[4 * k], v0.x, a0);
-    a1 = fma(m[4 * k + 1], v0.y, a1);
-    a0 = fma(m[4 * k + 2], v1.x, a0);
-    a1 = fma(m[4 * k + 3], v1.y, a1);
-  }
-  double acc = a0 + a1;
-  acc += __shfl_xor_sync(FULL, acc, 1);
-  acc += __shfl_xor_sync(FULL, acc, 2);
-  return acc;
-}
 __device__ __forceinline__ double warp_sumsq(const double* x) {
   const int lane = threadIdx.x & 31;
   double acc = 0.0;
@@ -105,21 +77,55 @@ __device__ __forceinline__ void put_code(uint32_t* w, int bit, int bits, uint32_
   if ((bit & 31) + bits > 32) atomicOr(w + (bit >> 5) + 1, code >> (32 - (bit & 31)));
 }
 
+// A warp's 16 rows of a row-major fp32 matrix as m16n8k4 fp64 A fragments: k-step kk: rows gq, gq + 8 of
+// column 4kk + t.
+struct Rows16 {
+  float m[32][2];
+  __device__ __forceinline__ void load(const float* M, int warp, int gq, int t) {
+#pragma unroll
+    for (int kk = 0; kk < 32; ++kk) {
+      m[kk][0] = __ldg(M + (16 * warp + gq) * D + 4 * kk + t);
+      m[kk][1] = __ldg(M + (16 * warp + gq + 8) * D + 4 * kk + t);
+    }
+  }
+  // Products with eight vectors (column n: x[n]), in fp64: d[0], d[1]: row gq of columns 2t, 2t + 1;
+  // d[2], d[3]: row gq + 8.
+  __device__ __forceinline__ void times(const double (*x)[XS], int gq, int t, double (&d)[4]) const {
+    double e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = e[i] = 0.0;
+#pragma unroll
+    for (int kk = 0; kk < 32; ++kk) {
+      const double b = x[gq][4 * kk + t];
+      double(&s)[4] = kk & 1 ? e : d;
+      asm("mma.sync.aligned.m16n8k4.row.col.f64.f64.f64.f64 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};\n"
+          : "+d"(s[0]), "+d"(s[1]), "+d"(s[2]), "+d"(s[3])
+          : "d"((double)m[kk][0]), "d"((double)m[kk][1]), "d"(b));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] += e[i];
+  }
+};
+
 __global__ void __launch_bounds__(QT, 1) quantize_rows(const __grid_constant__ RowArgs a) {
   __shared__ RowSmem s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int j = tid >> 2, q = tid & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, t = lane & 3;
   const int64_t r0 = (int64_t)blockIdx.x * a.rows;
   const int nr = (int)min((int64_t)a.rows, (int64_t)a.N * a.Hkv - r0);
-  double m[32];
-  load_quarter(a.Pi, j, q, m);
-  for (int i = tid; i < 2 * nr * D; i += QT) {
-    const int v = i / D, e = i % D, row = v < nr ? v : v - nr;
-    const int64_t n = (r0 + row) / a.Hkv, h = (r0 + row) % a.Hkv;
-    const int64_t at = n * a.sn + h * a.sh + e;
-    const void* src = v < nr ? a.k : a.v;
-    s.x[v < nr ? row : ROWS + row][e] = a.in_f32 ? (double)reinterpret_cast<const float*>(src)[at]
-                                                : (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src)[at]);
+  Rows16 pi, sk;
+  pi.load(a.Pi, warp, gq, t);
+  if (a.qjl) sk.load(a.S, warp, gq, t);
+  for (int i = tid; i < 2 * ROWS * D; i += QT) {  // (columns without a row: zeros)
+    const int v = i / D, e = i % D, row = v % ROWS;
+    double x = 0.0;
+    if (row < nr) {
+      const int64_t n = (r0 + row) / a.Hkv, h = (r0 + row) % a.Hkv;
+      const int64_t at = n * a.sn + h * a.sh + e;
+      const void* src = v < ROWS ? a.k : a.v;
+      x = a.in_f32 ? (double)reinterpret_cast<const float*>(src)[at]
+                   : (double)__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(src)[at]);
+    }
+    s.x[v][e] = x;
   }
   if (tid < 16) s.kc[tid] = tid < (1 << a.k_bits) ? a.kc[tid] : 0.0f;
   else if (tid < 32) s.vc[tid - 16] = tid - 16 < (1 << a.v_bits) ? a.vc[tid - 16] : 0.0f;
@@ -128,40 +134,42 @@ __global__ void __launch_bounds__(QT, 1) quantize_rows(const __grid_constant__ R
   for (int i = tid; i < ROWS * 36; i += QT) (&s.kw[0][0])[i] = 0u;  // kw, vw and sw lie together
   static_assert(offsetof(RowSmem, sw) - offsetof(RowSmem, kw) == ROWS * 32 * 4, "packed rows");
   __syncthreads();
-  if (warp < 2 * ROWS && warp % ROWS < nr) {
-    const double ss = warp_sumsq(s.x[warp]);
+  {
+    const double ss = warp_sumsq(s.x[warp]);  // eight warps, eight vectors
     if (lane == 0) s.n[warp] = sqrt(ss);
   }
-  __syncthreads();
   const double sqd = sqrt((double)D);
-  for (int v = 0; v < 2 * nr; ++v) {  // keys, then values
-    const bool isv = v >= nr;
-    const int row = isv ? v - nr : v;
-    const double y = dot_quarter(m, s.x[isv ? ROWS + row : row], q);
-    if (q != (v & 3)) continue;
-    const double n = s.n[isv ? ROWS + row : row];
+  double d[4];
+  pi.times(s.x, gq, t, d);
+  __syncthreads();  // the norms
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int v = 2 * t + (i & 1), j = 16 * warp + gq + 8 * (i >> 1), row = v % ROWS;
+    const bool isv = v >= ROWS;
+    const double n = s.n[v];
     // a zero row, or one with infinities or NaN, has the codes of u = 0
-    const double u = n > 0.0 && n < INFINITY ? sqd * y / n : 0.0;
+    const double u = n > 0.0 && n < INFINITY ? sqd * d[i] / n : 0.0;
     const float* th = isv ? s.vt : s.kt;
     uint32_t idx = 0;
 #pragma unroll
     for (int c = 0; c < 15; ++c) idx += u >= (double)th[c] ? 1u : 0u;
-    if (!isv) s.rho[row][j] = u - (double)s.kc[idx];
+    s.rho[v][j] = isv ? 0.0 : u - (double)s.kc[idx];
     const int bits = isv ? a.v_bits : a.k_bits;
     put_code(isv ? s.vw[row] : s.kw[row], bits * (isv ? v_slot_of_coord(j) : k_slot_of_coord(j)), bits, idx);
   }
-  if (a.qjl) load_quarter(a.S, j, q, m);
   __syncthreads();
   if (a.qjl) {
-    if (warp < nr) {
+    if (warp < ROWS) {
       const double ss = warp_sumsq(s.rho[warp]);
       if (lane == 0) s.r2[warp] = ss;
     }
-    for (int row = 0; row < nr; ++row) {
-      const double y = dot_quarter(m, s.rho[row], q);
-      if (q == (row & 3) && y >= 0.0) {
-        const int bit = sign_bit_of_row(j);
-        atomicOr(&s.sw[row][bit >> 5], 1u << (bit & 31));
+    sk.times(s.rho, gq, t, d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = 2 * t + (i & 1), l = 16 * warp + gq + 8 * (i >> 1);
+      if (v < ROWS && d[i] >= 0.0) {
+        const int bit = sign_bit_of_row(l);
+        atomicOr(&s.sw[v][bit >> 5], 1u << (bit & 31));
       }
     }
     __syncthreads();
@@ -215,6 +223,13 @@ __device__ __forceinline__ uint32_t bits_at(const uint8_t* row, int bit) {
   uint32_t w = p[0];
   if (LEN > 8 || sh + LEN > 8) w |= (uint32_t)p[1] << 8;
   return (w >> sh) & ((1u << LEN) - 1u);
+}
+
+// Table value of the code at bit `sh` of w.
+template <int BITS>
+__device__ __forceinline__ float entry(const float* table, uint32_t w, int sh) {
+  const uint32_t at = (sh >= 2 ? w >> (sh - 2) : w << (2 - sh)) & (((1u << BITS) - 1u) << 2);
+  return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(table) + at);
 }
 
 template <typename T>
@@ -275,24 +290,23 @@ __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs
   for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int x = 0; x < 4; ++x)  // slot 32t + 4p + x is coordinate 16p + 8 (x / 2) + 2t + x % 2
-      v[8 * (x >> 1) + 2 * t + (x & 1)] = kc[(kq[t] >> (KB * x)) & ((1u << KB) - 1u)] * kn;
+      v[8 * (x >> 1) + 2 * t + (x & 1)] = entry<KB>(kc, kq[t], KB * x) * kn;
   store16(reinterpret_cast<T*>(a.k_out) + r * D + 16 * p, v);
 #pragma unroll
   for (int g = 0; g < 8; ++g)
 #pragma unroll
     for (int x = 0; x < 2; ++x)  // slot 16g + 2p + x is coordinate 16p + 8x + g
-      v[8 * x + g] = vc[(vq[g] >> (VB * x)) & ((1u << VB) - 1u)] * vn;
+      v[8 * x + g] = entry<VB>(vc, vq[g], VB * x) * vn;
   store16(reinterpret_cast<T*>(a.v_out) + r * D + 16 * p, v);
   if (a.signs) {
     // sketch row 16p + 8h + 2t + e is bit 2p + h + 16e of word t: byte 1 or -1 (0: no row)
-    const uint32_t w[4] = {sg.x, sg.y, sg.z, sg.w};
-    uint32_t o[4] = {0, 0, 0, 0};
-    if (row >= 0) {
+    const uint32_t w[4] = {sg.x >> (2 * p), sg.y >> (2 * p), sg.z >> (2 * p), sg.w >> (2 * p)};
+    uint32_t o[4];
 #pragma unroll
-      for (int l = 0; l < 16; ++l) {
-        const int h = l >> 3, t = (l >> 1) & 3, e = l & 1;
-        o[l >> 2] |= ((w[t] >> (2 * p + h + 16 * e)) & 1u ? 0x01u : 0xffu) << (8 * (l & 3));
-      }
+    for (int k = 0; k < 4; ++k) {  // four rows: h = k / 2, words 2 (k % 2) and + 1, e = 0, 1
+      const uint32_t x = (w[2 * (k & 1)] >> (k >> 1)) & 0x00010001u, y = (w[2 * (k & 1) + 1] >> (k >> 1)) & 0x00010001u;
+      const uint32_t v = __byte_perm(x, y, 0x6420);
+      o[k] = row >= 0 ? v | ((v ^ 0x01010101u) * 255u) : 0u;
     }
     reinterpret_cast<uint4*>(a.signs)[r * 8 + p] = make_uint4(o[0], o[1], o[2], o[3]);
   }

@@ -87,34 +87,45 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& total) {
   return part[warp] + x - v;
 }
 
-// The first `need` free pages in order to room[]; returns how many there are (at most need + what
-// the last chunk holds).  Four pages per thread and round.
+// The plan's threads take contiguous shares of the pages, whole 16-byte words: share [begin, end) of
+// thread tid.  (A share per thread needs one scan over the CTA, where chunks of 4096 pages in turn took
+// one each: 18 us for 16K pages.)
+__device__ __forceinline__ void share_of(int pages, int& begin, int& end) {
+  const int per = (pages + 4 * PLAN_THREADS - 1) / (4 * PLAN_THREADS) * 4;
+  begin = (int)min((int64_t)threadIdx.x * per, (int64_t)pages);
+  end = min(begin + per, pages);
+}
+// f(p, refs[p]) for the pages of a share, four to a load.
+template <typename F>
+__device__ __forceinline__ void each_page(const int32_t* refs, int begin, int end, F&& f) {
+  int p = begin;
+#pragma unroll 2
+  for (; p + 4 <= end; p += 4) {
+    const int4 r = *reinterpret_cast<const int4*>(refs + p);
+    f(p, r.x);
+    f(p + 1, r.y);
+    f(p + 2, r.z);
+    f(p + 3, r.w);
+  }
+  for (; p < end; ++p) f(p, refs[p]);
+}
+
+// The first `need` free pages in order to room[]; returns how many free pages there are.
 __device__ int64_t free_pages(const tq_page_table& pt, int64_t need, int32_t* room) {
-  int64_t found = 0;
-  for (int base = 0; base < pt.num_pages && found < need; base += 4 * PLAN_THREADS) {
-    const int p0 = base + 4 * threadIdx.x;
-    bool f[4];
-    if (p0 + 4 <= pt.num_pages) {
-      const int4 r = *reinterpret_cast<const int4*>(pt.refs + p0);
-      f[0] = r.x <= 0;
-      f[1] = r.y <= 0;
-      f[2] = r.z <= 0;
-      f[3] = r.w <= 0;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = p0 + j < pt.num_pages && pt.refs[p0 + j] <= 0;
-    }
-    int64_t total;
-    int64_t at = found + block_scan((int)f[0] + (int)f[1] + (int)f[2] + (int)f[3], total);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (f[j]) {
-        if (at < need) room[at] = p0 + j;
+  int begin, end;
+  share_of(pt.num_pages, begin, end);
+  int mine = 0;
+  each_page(pt.refs, begin, end, [&](int, int r) { mine += r <= 0; });
+  int64_t total;
+  int64_t at = block_scan(mine, total);
+  if (mine && at < need)
+    each_page(pt.refs, begin, end, [&](int p, int r) {
+      if (r <= 0) {
+        if (at < need) room[at] = p;
         ++at;
       }
-    found += total;
-  }
-  return found;
+    });
+  return total;
 }
 
 // The entry i of a list whose prefix sums are off[0..n] that holds unit u: the last i with off[i] <= u
@@ -399,34 +410,41 @@ __global__ void __launch_bounds__(COPY_THREADS) free_seqs(const tq_page_table pt
 __global__ void __launch_bounds__(PLAN_THREADS) compact_plan(const tq_page_table pt, int32_t* wsp) {
   const Ws w = ws_at(wsp, 0, pt.n_seq, pt.num_pages);
   const int tid = threadIdx.x, P = pt.num_pages;
+  __shared__ int below;  // pages in use with a number below `live`
   pdl_launch();
-  int64_t mine = 0, live;
-  for (int p = tid; p < P; p += PLAN_THREADS) {
-    mine += pt.refs[p] > 0;
-    w.map[p] = p;
-  }
-  block_scan(mine, live);
-  // free numbers below `live` (to) and pages in use from `live` on (from), each in order
-  int64_t holes = 0, movers = 0;
-  for (int base = 0; base < P; base += PLAN_THREADS) {
-    const int p = base + tid;
-    const bool used = p < P && pt.refs[p] > 0;
-    const bool hole = p < P && p < live && !used, move = used && p >= live;
-    int64_t both;  // the two counts in one scan
-    const int64_t at = block_scan((hole ? 1 : 0) + (move ? (int64_t)1 << 32 : 0), both);
-    if (hole) w.to[holes + (int32_t)(at & 0xffffffff)] = p;
-    if (move) w.from[movers + (int32_t)(at >> 32)] = p;
-    holes += both & 0xffffffff;
-    movers += both >> 32;
+  int begin, end, mine = 0;
+  share_of(P, begin, end);
+  each_page(pt.refs, begin, end, [&](int, int r) { mine += r > 0; });
+  int64_t live;
+  const int before = (int)block_scan(mine, live);  // pages in use before the share
+  if (live == P && tid == 0) below = (int)live;
+  if (begin <= live && live < end) {
+    int n = before;
+    each_page(pt.refs, begin, (int)live, [&](int, int r) { n += r > 0; });
+    below = n;
   }
   __syncthreads();
-  for (int i = tid; i < (int)movers; i += PLAN_THREADS) {  // (as many holes as movers)
+  // free numbers below `live` (to) and pages in use from `live` on (from), each in order: as many of
+  // the ones as of the others
+  const int movers = (int)live - below;
+  int n = before;
+  each_page(pt.refs, begin, end, [&](int p, int r) {
+    w.map[p] = p;
+    if (r > 0) {
+      if (p >= live) w.from[n - below] = p;
+      ++n;
+    } else if (p < live) {
+      w.to[p - n] = p;
+    }
+  });
+  __syncthreads();
+  for (int i = tid; i < movers; i += PLAN_THREADS) {
     const int s = w.from[i], d = w.to[i];
     w.map[s] = d;
     pt.refs[d] = pt.refs[s];
     pt.refs[s] = 0;
   }
-  if (tid == 0) w.head[0] = (int32_t)movers;
+  if (tid == 0) w.head[0] = movers;
 }
 
 __global__ void __launch_bounds__(COPY_THREADS)

@@ -1,14 +1,15 @@
 // tq_rope: rotary positions of queries and keys with one or several position axes.
 //
-// Pair i of every head of token n turns by t = pos[axis(i)][n] * base^(-2i/128).  Everything a
-// token's heads need is 64 angles, so a CTA takes a few tokens at a time: 64 threads per token turn
-// positions into (cos, sin) in shared memory while every thread's first loads of q and k are already
-// under way, then the heads stream through in 16-byte loads and stores.
+// Pair i of every head of token n turns by t = pos[axis(i)][n] * base^(-2i/128).  A token's heads share
+// its 64 angles, so 64 threads take a token: each turns one position into (cos, sin), and, after one
+// barrier, keeps those of the pairs it works on in registers for all the heads it passes (every 8th, or
+// every 4th in fp32).  All loads of a thread's first heads are under way before the angles are formed.
 //
 // The angle is formed in turns, pos * (base^(-2i/128) / 2 pi), in fp64 and reduced to [-1/2, 1/2]
 // before it becomes fp32 for sincospi: at position 2^20 an fp32 product would be off by 0.06 rad.
 // The rotation itself is fp32, rounded once to the output's type.  Bound by memory: every element is
-// read and written once.
+// read and written once.  (Items spread over a CTA's threads by division, each reading its (cos, sin) from
+// shared memory, took 67 us for 16384 tokens of 40 bf16 heads, bound by their instructions.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,16 +23,15 @@ namespace {
 
 constexpr int D = kHeadDim;
 constexpr int PAIRS = D / 2;
-constexpr int THREADS = 256;
-constexpr int TOK_MAX = 4;   // tokens of a CTA
-constexpr int PRE = 4;       // work items a thread has loads in flight for
+constexpr int TOK = 4;       // tokens of a CTA
+constexpr int PRE = 5;       // heads a thread has loads in flight for
 
 struct RopeArgs {
   const void* x[2];          // q, k
   void* y[2];
   int64_t sn[2], sh[2];      // input strides (elements)
   int H[2];
-  int N, tok, axes;
+  int N;
   const int32_t* pos;
   int64_t pos_stride;
   float sign;                // -1: inverse
@@ -77,90 +77,84 @@ struct Vec<float> {
   }
 };
 
-// A work item is two 16-byte vectors of one head: coordinates c N .. and 64 + c N .. (HALF), or
-// 2 c N .. in sequence (PAIR); V = items per head.
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeArgs a) {
+// V threads share a head: thread c works on its pairs c E .. c E + E - 1: the 16-byte vectors c and c + V
+// (HALF), or 2c and 2c + 1 (PAIR).  A CTA has T tokens, 64 threads each.
+template <typename T, bool HALF, int TK>
+__global__ void __launch_bounds__(PAIRS * TK) rope_kernel(const __grid_constant__ RopeArgs a) {
   using Vc = Vec<T>;
-  constexpr int E = Vc::N, V = PAIRS / E;
-  __shared__ float2 cs[TOK_MAX][PAIRS];
-  const int tid = threadIdx.x;
-  const int n0 = blockIdx.x * a.tok, nt = min(a.tok, a.N - n0);
-  const int per_tok = (a.H[0] + a.H[1]) * V, total = nt * per_tok;
-  // item -> input and output vectors
-  auto where = [&](int item, const uint4*& src, uint4*& dst, int& tok, int& c) {
-    tok = item / per_tok;
-    int r = item - tok * per_tok;
-    c = r % V;
-    int h = r / V;
-    const int which = h < a.H[0] ? 0 : 1;
-    h -= which ? a.H[0] : 0;
-    const int64_t n = n0 + tok;
-    src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.x[which]) + n * a.sn[which] + h * a.sh[which]);
-    dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.y[which]) + (n * a.H[which] + h) * D);
-  };
-  constexpr int STEP = HALF ? V : 1;  // vectors between an item's two
-  auto first = [](int c) { return HALF ? c : 2 * c; };
-
+  constexpr int E = Vc::N, V = PAIRS / E, HS = PAIRS / V;  // HS: heads at a time
+  __shared__ float2 cs[TK][PAIRS];
+  const int tok = threadIdx.x / PAIRS, i64 = threadIdx.x % PAIRS, c = i64 % V, h0 = i64 / V;
+  const int n = blockIdx.x * TK + tok;
+  const int H = n < a.N ? a.H[0] + a.H[1] : 0;
+  constexpr int STEP = HALF ? V : 1;
+  const int first = HALF ? c : 2 * c;
+  const T* in[2] = {reinterpret_cast<const T*>(a.x[0]) + (int64_t)n * a.sn[0], reinterpret_cast<const T*>(a.x[1]) + (int64_t)n * a.sn[1]};
+  T* out[2] = {reinterpret_cast<T*>(a.y[0]) + (int64_t)n * a.H[0] * D, reinterpret_cast<T*>(a.y[1]) + (int64_t)n * a.H[1] * D};
   uint4 lo[PRE], hi[PRE];
+  auto load = [&](int p, int h) {
+    const uint4* src = reinterpret_cast<const uint4*>(h < a.H[0] ? in[0] + h * a.sh[0] : in[1] + (h - a.H[0]) * a.sh[1]) + first;
+    lo[p] = src[0];
+    hi[p] = src[STEP];
+  };
 #pragma unroll
-  for (int p = 0; p < PRE; ++p) {
-    const int item = tid + p * THREADS;
-    if (item < total) {
-      const uint4* src;
-      uint4* dst;
-      int tok, c;
-      where(item, src, dst, tok, c);
-      lo[p] = src[first(c)];
-      hi[p] = src[first(c) + STEP];
-    }
-  }
-  for (int i = tid; i < nt * PAIRS; i += THREADS) {
-    const int tok = i / PAIRS, p = i % PAIRS;
-    const double t = (double)a.pos[a.axis[p] * a.pos_stride + n0 + tok] * a.turns[p];
-    float s, c;
-    sincospif(2.0f * (float)(t - rint(t)), &s, &c);
-    cs[tok][p] = make_float2(c, a.sign * s);
+  for (int p = 0; p < PRE; ++p)
+    if (h0 + p * HS < H) load(p, h0 + p * HS);
+  if (n < a.N) {
+    const double t = (double)a.pos[a.axis[i64] * a.pos_stride + n] * a.turns[i64];
+    float s, co;
+    sincospif(2.0f * (float)(t - rint(t)), &s, &co);
+    cs[tok][i64] = make_float2(co, a.sign * s);
   }
   __syncthreads();
-  for (int base = 0; base < total; base += PRE * THREADS) {
+  float2 w[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) w[i] = cs[tok][c * E + i];
+  for (int hb = h0; hb < H; hb += PRE * HS) {
 #pragma unroll
     for (int p = 0; p < PRE; ++p) {
-      const int item = base + tid + p * THREADS;
-      if (item >= total) break;
-      const uint4* src;
-      uint4* dst;
-      int tok, c;
-      where(item, src, dst, tok, c);
+      const int h = hb + p * HS;
+      if (h >= H) break;
       float x[E], y[E];
       Vc::unpack(lo[p], x);
       Vc::unpack(hi[p], y);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        const float2 w = cs[tok][c * E + i];
-        if constexpr (HALF) {  // (x[i], y[i]) is pair cE + i
-          const float u = x[i];
-          x[i] = fmaf(u, w.x, -(y[i] * w.y));
-          y[i] = fmaf(u, w.y, y[i] * w.x);
-        } else {               // the 2E coordinates in sequence are pairs cE ..
-          float& u = 2 * i < E ? x[(2 * i) % E] : y[(2 * i) % E];
-          float& v = 2 * i < E ? x[(2 * i + 1) % E] : y[(2 * i + 1) % E];
-          const float u0 = u;
-          u = fmaf(u0, w.x, -(v * w.y));
-          v = fmaf(u0, w.y, v * w.x);
-        }
+        // HALF: (x[i], y[i]) is pair cE + i; PAIR: the 2E coordinates in sequence are pairs cE ..
+        float& u = HALF ? x[i] : 2 * i < E ? x[(2 * i) % E] : y[(2 * i) % E];
+        float& v = HALF ? y[i] : 2 * i < E ? x[(2 * i + 1) % E] : y[(2 * i + 1) % E];
+        const float u0 = u;
+        u = fmaf(u0, w[i].x, -(v * w[i].y));
+        v = fmaf(u0, w[i].y, v * w[i].x);
       }
-      dst[first(c)] = Vc::pack(x);
-      dst[first(c) + STEP] = Vc::pack(y);
-      // the item this register pair takes next
-      const int next = item + PRE * THREADS;
-      if (next < total) {
-        where(next, src, dst, tok, c);
-        lo[p] = src[first(c)];
-        hi[p] = src[first(c) + STEP];
-      }
+      uint4* dst = reinterpret_cast<uint4*>(h < a.H[0] ? out[0] + h * D : out[1] + (h - a.H[0]) * D) + first;
+      dst[0] = Vc::pack(x);
+      dst[STEP] = Vc::pack(y);
+      if (h + PRE * HS < H) load(p, h + PRE * HS);
     }
   }
+}
+
+template <typename T, bool HALF>
+void launch_rope(const RopeArgs& a, int sms, cudaStream_t s) {
+  // one token per CTA while those do not fill the SMs' CTA slots
+  if (a.N <= 8 * sms) rope_kernel<T, HALF, 1><<<a.N, PAIRS, 0, s>>>(a);
+  else rope_kernel<T, HALF, TOK><<<(a.N + TOK - 1) / TOK, PAIRS * TOK, 0, s>>>(a);
+}
+
+// base^(-2i/128) / (2 pi) for all pairs: six square roots and products of their powers in extended
+// precision, rounded once (64 calls of pow would take as long as the launch).
+void turns_of(double base, double (&turns)[PAIRS]) {
+  long double root[6];  // base^(-2^k / 64)
+  root[5] = 1.0L / sqrtl((long double)base);
+  for (int k = 4; k >= 0; --k) root[k] = sqrtl(root[k + 1]);
+  long double p[PAIRS];
+  p[0] = 1.0L;
+  for (int i = 1; i < PAIRS; ++i) {
+    const int k = 31 - __builtin_clz(i);
+    p[i] = p[i - (1 << k)] * root[k];
+  }
+  for (int i = 0; i < PAIRS; ++i) turns[i] = (double)(p[i] / (2.0L * 3.14159265358979323846264338327950288L));
 }
 
 }  // namespace
@@ -196,11 +190,11 @@ extern "C" tq_status tq_rope(const void* q, int64_t q_stride_n, int64_t q_stride
     if (x[w] == y[w] && !packed)
       return fail(TQ_ERR_INVALID_ARG, "in place needs a contiguous input");
   }
-  RopeArgs a = {};
+  RopeArgs a;
+  turns_of(base, a.turns);
   for (int i = 0; i < PAIRS; ++i) {
     if (axis_of_pair[i] >= axes) return fail(TQ_ERR_INVALID_ARG, "axis_of_pair[%d] = %d of %d axes", i, axis_of_pair[i], axes);
     a.axis[i] = axis_of_pair[i];
-    a.turns[i] = std::pow(base, -2.0 * i / kHeadDim) / (2.0 * M_PI);
   }
   if (N == 0 || Hq + Hkv == 0) return TQ_OK;
   for (int w = 0; w < 2; ++w) {
@@ -211,20 +205,19 @@ extern "C" tq_status tq_rope(const void* q, int64_t q_stride_n, int64_t q_stride
     a.H[w] = H[w];
   }
   a.N = N;
-  a.axes = axes;
   a.pos = pos;
   a.pos_stride = pos_stride;
   a.sign = inverse ? -1.0f : 1.0f;
-  // one token per CTA while that still fills the SMs' threads once, else TOK_MAX
-  a.tok = N <= 1184 ? 1 : TOK_MAX;
-  const int grid = (N + a.tok - 1) / a.tok;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    cudaGetLastError();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == TQ_BF16) {
-    if (style == TQ_ROPE_HALF) rope_kernel<__nv_bfloat16, true><<<grid, THREADS, 0, s>>>(a);
-    else rope_kernel<__nv_bfloat16, false><<<grid, THREADS, 0, s>>>(a);
+    if (style == TQ_ROPE_HALF) launch_rope<__nv_bfloat16, true>(a, sms, s);
+    else launch_rope<__nv_bfloat16, false>(a, sms, s);
   } else {
-    if (style == TQ_ROPE_HALF) rope_kernel<float, true><<<grid, THREADS, 0, s>>>(a);
-    else rope_kernel<float, false><<<grid, THREADS, 0, s>>>(a);
+    if (style == TQ_ROPE_HALF) launch_rope<float, true>(a, sms, s);
+    else launch_rope<float, false>(a, sms, s);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));

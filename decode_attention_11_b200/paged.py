@@ -84,7 +84,7 @@ def _rope_arg(x: Optional[torch.Tensor], out: Optional[torch.Tensor], name: str,
     if x.dim() != 3 or x.shape[0] != N or x.shape[2] != 128 or x.stride(2) != 1:
         raise ValueError(f"{name} must be [N, H, 128] with a contiguous last dim, N = {N}")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(N, x.shape[1], 128, dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
         raise ValueError(f"{name}_out must be contiguous, of the shape and dtype of {name}")
     sn, sh, _ = x.stride()
