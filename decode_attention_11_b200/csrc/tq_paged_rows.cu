@@ -77,16 +77,16 @@ __device__ __forceinline__ void put_code(uint32_t* w, int bit, int bits, uint32_
   if ((bit & 31) + bits > 32) atomicOr(w + (bit >> 5) + 1, code >> (32 - (bit & 31)));
 }
 
-// A warp's 16 rows of a row-major fp32 matrix as m16n8k4 fp64 A fragments: k-step kk: rows gq, gq + 8 of
-// column 4kk + t.
+// A warp's 16 rows of a row-major fp32 matrix as m16n8k4 fp64 A fragments.  The order of the k-steps'
+// columns is free: step 4m + i of lane t takes column 16m + 4t + i, so that a lane loads and reads four
+// columns at a time.
 struct Rows16 {
-  float m[32][2];
+  float4 m[8][2];  // rows gq, gq + 8
   __device__ __forceinline__ void load(const float* M, int warp, int gq, int t) {
 #pragma unroll
-    for (int kk = 0; kk < 32; ++kk) {
-      m[kk][0] = __ldg(M + (16 * warp + gq) * D + 4 * kk + t);
-      m[kk][1] = __ldg(M + (16 * warp + gq + 8) * D + 4 * kk + t);
-    }
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) m[k][r] = __ldg(reinterpret_cast<const float4*>(M + (16 * warp + gq + 8 * r) * D + 16 * k + 4 * t));
   }
   // Products with eight vectors (column n: x[n]), in fp64: d[0], d[1]: row gq of columns 2t, 2t + 1;
   // d[2], d[3]: row gq + 8.
@@ -94,13 +94,19 @@ struct Rows16 {
     double e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) d[i] = e[i] = 0.0;
-#pragma unroll
-    for (int kk = 0; kk < 32; ++kk) {
-      const double b = x[gq][4 * kk + t];
-      double(&s)[4] = kk & 1 ? e : d;
+    auto step = [](double (&s)[4], float a0, float a1, double b) {
       asm("mma.sync.aligned.m16n8k4.row.col.f64.f64.f64.f64 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};\n"
           : "+d"(s[0]), "+d"(s[1]), "+d"(s[2]), "+d"(s[3])
-          : "d"((double)m[kk][0]), "d"((double)m[kk][1]), "d"(b));
+          : "d"((double)a0), "d"((double)a1), "d"(b));
+    };
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const double2 b0 = *reinterpret_cast<const double2*>(&x[gq][16 * k + 4 * t]);
+      const double2 b1 = *reinterpret_cast<const double2*>(&x[gq][16 * k + 4 * t + 2]);
+      step(d, m[k][0].x, m[k][1].x, b0.x);
+      step(e, m[k][0].y, m[k][1].y, b0.y);
+      step(d, m[k][0].z, m[k][1].z, b1.x);
+      step(e, m[k][0].w, m[k][1].w, b1.y);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) d[i] += e[i];
@@ -215,16 +221,6 @@ struct ReadArgs {
   float* rnorm;
 };
 
-// `len` (<= 16) bits at bit `bit` of a row, by bytes (the second only where the bits reach it).
-template <int LEN>
-__device__ __forceinline__ uint32_t bits_at(const uint8_t* row, int bit) {
-  const uint8_t* p = row + (bit >> 3);
-  const int sh = bit & 7;
-  uint32_t w = p[0];
-  if (LEN > 8 || sh + LEN > 8) w |= (uint32_t)p[1] << 8;
-  return (w >> sh) & ((1u << LEN) - 1u);
-}
-
 // Table value of the code at bit `sh` of w.
 template <int BITS>
 __device__ __forceinline__ float entry(const float* table, uint32_t w, int sh) {
@@ -255,49 +251,62 @@ constexpr int RT = 256;
 template <int KB, int VB, typename T>
 __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs a) {
   __shared__ float kc[16], vc[16];
-  if (threadIdx.x < 16) kc[threadIdx.x] = threadIdx.x < (1 << KB) ? a.kc[threadIdx.x] : 0.0f;
-  else if (threadIdx.x < 32) vc[threadIdx.x - 16] = threadIdx.x - 16 < (1 << VB) ? a.vc[threadIdx.x - 16] : 0.0f;
-  const int64_t r = ((int64_t)blockIdx.x * RT + threadIdx.x) >> 3;
+  const uint32_t r = (blockIdx.x * (uint32_t)RT + threadIdx.x) >> 3;  // (at most 2^30 rows)
   const int p = threadIdx.x & 7;
-  const bool live = r < (int64_t)a.N * a.Hkv;
+  const bool live = r < (uint32_t)a.N * (uint32_t)a.Hkv;
   int64_t row = -1;
   if (live) {
-    const int n = (int)(r / a.Hkv);
-    row = slot_row(a.slots[n], (int)(r - (int64_t)n * a.Hkv), a.Hkv, a.pages, a.ps);
+    const uint32_t n = r / (uint32_t)a.Hkv;
+    row = slot_row(a.slots[n], (int)(r - n * a.Hkv), a.Hkv, a.pages, a.ps);
   }
+  if (threadIdx.x < 16) kc[threadIdx.x] = threadIdx.x < (1 << KB) ? a.kc[threadIdx.x] : 0.0f;
+  else if (threadIdx.x < 32) vc[threadIdx.x - 16] = threadIdx.x - 16 < (1 << VB) ? a.vc[threadIdx.x - 16] : 0.0f;
+  __syncthreads();
+  if (!live) return;
   uint32_t kq[4] = {0, 0, 0, 0}, vq[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   uint4 sg = make_uint4(0, 0, 0, 0);
   float kn = 0.0f, vn = 0.0f, rn = 0.0f;
   if (row >= 0) {
-    const uint8_t* kr = a.k_codes + row * (16 * KB);
-    const uint8_t* vr = a.v_codes + row * (16 * VB);
+    // key codes: 4 KB bits at bit KB (32t + 4p); value codes: 2 VB bits at bit VB (16g + 2p)
+    const uint8_t* kr = a.k_codes + row * (16 * KB) + (4 * KB * p) / 8;
+    const uint8_t* vr = a.v_codes + row * (16 * VB) + (2 * VB * p) / 8;
+    const int ks = (4 * KB * p) & 7, vs = (2 * VB * p) & 7;
+    const bool v2 = VB == 3 && vs + 6 > 8;  // the field goes on in the next byte
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      if constexpr (KB == 4) kq[t] = *reinterpret_cast<const uint16_t*>(kr + 16 * t + 2 * p);
-      else kq[t] = bits_at<4 * KB>(kr, KB * (32 * t + 4 * p));
+      if constexpr (KB == 4) kq[t] = *reinterpret_cast<const uint16_t*>(kr + 16 * t);
+      else if constexpr (KB == 2) kq[t] = kr[8 * t];
+      else kq[t] = (uint32_t)kr[12 * t] | (uint32_t)kr[12 * t + 1] << 8;
     }
 #pragma unroll
-    for (int g = 0; g < 8; ++g) vq[g] = bits_at<2 * VB>(vr, VB * (16 * g + 2 * p));
+    for (int g = 0; g < 8; ++g) {
+      vq[g] = vr[2 * VB * g];
+      if (VB == 3 && v2) vq[g] |= (uint32_t)vr[2 * VB * g + 1] << 8;
+    }
+    if (a.signs) sg = *reinterpret_cast<const uint4*>(a.k_signs + row * 16);
     kn = a.k_norm[row] * 0.08838834764831845f;  // 1 / sqrt(128)
     vn = a.v_norm[row] * 0.08838834764831845f;
-    if (a.signs) sg = *reinterpret_cast<const uint4*>(a.k_signs + row * 16);
     if (a.rnorm) rn = a.k_rnorm[row];
+    if constexpr (KB == 3)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) kq[t] >>= ks;
+    if constexpr (VB != 4)
+#pragma unroll
+      for (int g = 0; g < 8; ++g) vq[g] >>= vs;
   }
-  __syncthreads();
-  if (!live) return;
   float v[16];
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int x = 0; x < 4; ++x)  // slot 32t + 4p + x is coordinate 16p + 8 (x / 2) + 2t + x % 2
       v[8 * (x >> 1) + 2 * t + (x & 1)] = entry<KB>(kc, kq[t], KB * x) * kn;
-  store16(reinterpret_cast<T*>(a.k_out) + r * D + 16 * p, v);
+  store16(reinterpret_cast<T*>(a.k_out) + (int64_t)r * D + 16 * p, v);
 #pragma unroll
   for (int g = 0; g < 8; ++g)
 #pragma unroll
     for (int x = 0; x < 2; ++x)  // slot 16g + 2p + x is coordinate 16p + 8x + g
       v[8 * x + g] = entry<VB>(vc, vq[g], VB * x) * vn;
-  store16(reinterpret_cast<T*>(a.v_out) + r * D + 16 * p, v);
+  store16(reinterpret_cast<T*>(a.v_out) + (int64_t)r * D + 16 * p, v);
   if (a.signs) {
     // sketch row 16p + 8h + 2t + e is bit 2p + h + 16e of word t: byte 1 or -1 (0: no row)
     const uint32_t w[4] = {sg.x >> (2 * p), sg.y >> (2 * p), sg.z >> (2 * p), sg.w >> (2 * p)};
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs
       const uint32_t v = __byte_perm(x, y, 0x6420);
       o[k] = row >= 0 ? v | ((v ^ 0x01010101u) * 255u) : 0u;
     }
-    reinterpret_cast<uint4*>(a.signs)[r * 8 + p] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(a.signs)[(int64_t)r * 8 + p] = make_uint4(o[0], o[1], o[2], o[3]);
   }
   if (a.rnorm && p == 0) a.rnorm[r] = rn;
 }

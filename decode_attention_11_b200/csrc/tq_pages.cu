@@ -36,7 +36,7 @@ struct Ws {
   int32_t* room;   // [num_pages] free pages in order
   int32_t* from;   // [max(n, num_pages)] copy pairs
   int32_t* to;
-  int32_t* map;    // [num_pages] new number of a page
+  int32_t* map;    // [num_pages] the page, or -1 - its place in from[]
 };
 __host__ __device__ inline size_t ws_words(int n, int n_seq, int pages) {
   const size_t pairs = n > pages ? n : pages;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(PLAN_THREADS)
   const Ws w = ws_at(wsp, n, pt.n_seq, pt.num_pages);
   __shared__ int bad;
   const int tid = threadIdx.x, ps = pt.page_size;
-  if (n_slots > 0) pdl_launch();  // only when the launch that follows is this call's own
+  pdl_launch();
   if (tid == 0) bad = 0;
   for (int i = tid; i < pt.n_seq; i += PLAN_THREADS) w.mark[i] = 0;
   __syncthreads();
@@ -210,28 +210,28 @@ __global__ void __launch_bounds__(PLAN_THREADS)
     w.head[1] = bad == 0;
     if (bad) atomicOr(pt.status, bad);
   }
-  if (bad) return;
-  for (int u = tid; u < (int)need; u += PLAN_THREADS) {
-    const int i = entry_of(w.need, n, u);
-    const int p = w.room[u];
-    pt.table[(int64_t)seqs[i] * pt.max_pages + pages_of(w.old[i], ps) + u - w.need[i]] = p;
-    pt.refs[p] = 1;
-  }
-  for (int i = tid; i < n; i += PLAN_THREADS) pt.seq_lens[seqs[i]] = w.old[i] + grow[i];
 }
 
+// The new pages' table entries and counts, the new lengths and the slots.
 __global__ void __launch_bounds__(COPY_THREADS)
-    reserve_slots(const tq_page_table pt, const int32_t* seqs, int n, int32_t* slots, int n_slots, int32_t* wsp) {
+    reserve_apply(const tq_page_table pt, const int32_t* seqs, const int32_t* grow, int n, int32_t* slots, int n_slots, int32_t* wsp) {
   const Ws w = ws_at(wsp, n, pt.n_seq, pt.num_pages);
   pdl_wait();
   const bool ok = w.head[1] != 0;
-  const int toks = ok ? w.tok[n] : 0, ps = pt.page_size;
-  for (int t = blockIdx.x * COPY_THREADS + threadIdx.x; t < n_slots; t += gridDim.x * COPY_THREADS) {
+  const int toks = ok ? w.tok[n] : 0, need = ok ? w.need[n] : 0, ps = pt.page_size;
+  const int first = blockIdx.x * COPY_THREADS + threadIdx.x, step = gridDim.x * COPY_THREADS;
+  for (int u = first; u < need; u += step) {
+    const int i = entry_of(w.need, n, u), p = w.room[u];
+    pt.table[(int64_t)seqs[i] * pt.max_pages + pages_of(w.old[i], ps) + u - w.need[i]] = p;
+    pt.refs[p] = 1;
+  }
+  for (int i = first; ok && i < n; i += step) pt.seq_lens[seqs[i]] = w.old[i] + grow[i];
+  for (int t = first; t < n_slots; t += step) {
     int v = -1;
     if (t < toks) {
-      const int i = entry_of(w.tok, n, t);
-      const int pos = w.old[i] + t - w.tok[i];
-      v = pt.table[(int64_t)seqs[i] * pt.max_pages + pos / ps] * ps + pos % ps;
+      const int i = entry_of(w.tok, n, t), pos = w.old[i] + t - w.tok[i], page = pos / ps;
+      const int fresh = page - pages_of(w.old[i], ps);  // >= 0: one of the new pages; -1: the old last one
+      v = (fresh >= 0 ? w.room[w.need[i] + fresh] : pt.table[(int64_t)seqs[i] * pt.max_pages + page]) * ps + (pos - page * ps);
     }
     slots[t] = v;
   }
@@ -428,22 +428,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) compact_plan(const tq_page_table
   // the ones as of the others
   const int movers = (int)live - below;
   int n = before;
-  each_page(pt.refs, begin, end, [&](int p, int r) {
-    w.map[p] = p;
+  auto one = [&](int p, int r) {  // (map: the page itself, or -1 - its place among the movers)
+    int m = p;
     if (r > 0) {
-      if (p >= live) w.from[n - below] = p;
+      if (p >= live) {
+        w.from[n - below] = p;
+        m = -1 - (n - below);
+      }
       ++n;
     } else if (p < live) {
       w.to[p - n] = p;
     }
-  });
-  __syncthreads();
-  for (int i = tid; i < movers; i += PLAN_THREADS) {
-    const int s = w.from[i], d = w.to[i];
-    w.map[s] = d;
-    pt.refs[d] = pt.refs[s];
-    pt.refs[s] = 0;
-  }
+    return m;
+  };
+  each_page(pt.refs, begin, end, [&](int p, int r) { w.map[p] = one(p, r); });
   if (tid == 0) w.head[0] = movers;
 }
 
@@ -453,13 +451,17 @@ __global__ void __launch_bounds__(COPY_THREADS)
   pdl_wait();
   const int moved = w.head[0];
   if (moved == 0) return;
+  for (int i = blockIdx.x * COPY_THREADS + threadIdx.x; rows && i < moved; i += gridDim.x * COPY_THREADS) {
+    pt.refs[w.to[i]] = pt.refs[w.from[i]];
+    pt.refs[w.from[i]] = 0;
+  }
   const int64_t entries = (int64_t)pt.n_seq * pt.max_pages;
   for (int64_t i = (int64_t)blockIdx.x * COPY_THREADS + threadIdx.x; rows && i < entries;
        i += (int64_t)gridDim.x * COPY_THREADS) {
     const int p = pt.table[i];
     if ((unsigned)p >= (unsigned)pt.num_pages) continue;
     const int q = w.map[p];
-    if (q != p) pt.table[i] = q;
+    if (q < 0) pt.table[i] = w.to[-1 - q];
   }
   copy_pairs(a, w.from, w.to, moved, 0, nullptr);
 }
@@ -593,9 +595,11 @@ extern "C" tq_status tq_pages_reserve(const tq_page_table* pt, const int32_t* se
   int32_t* w = reinterpret_cast<int32_t*>(workspace);
   reserve_plan<<<1, PLAN_THREADS, 0, s>>>(*pt, seqs, new_tokens, n, n_slots, slots != nullptr, w);
   st = launched("reserve plan");
-  if (st != TQ_OK || n_slots == 0) return st;
-  return launch_after(reserve_slots, grid_for((n_slots + COPY_THREADS - 1) / COPY_THREADS), s, "reserve slots", *pt, seqs, n,
-                      slots, n_slots, w);
+  if (st != TQ_OK) return st;
+  // (the number of new pages is known to the device alone: at most all of the pool)
+  const int64_t items = std::max<int64_t>(n_slots, std::min<int64_t>(pt->num_pages, (int64_t)n * pt->max_pages));
+  return launch_after(reserve_apply, grid_for((std::max<int64_t>(items, n) + COPY_THREADS - 1) / COPY_THREADS), s, "reserve", *pt, seqs,
+                      new_tokens, n, slots, n_slots, w);
 }
 
 extern "C" tq_status tq_pages_fork(const tq_page_table* pt, const int32_t* src, const int32_t* dst, int n,

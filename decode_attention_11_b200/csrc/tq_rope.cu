@@ -83,7 +83,7 @@ template <typename T, bool HALF, int TK>
 __global__ void __launch_bounds__(PAIRS * TK) rope_kernel(const __grid_constant__ RopeArgs a) {
   using Vc = Vec<T>;
   constexpr int E = Vc::N, V = PAIRS / E, HS = PAIRS / V;  // HS: heads at a time
-  __shared__ float2 cs[TK][PAIRS];
+  __shared__ __align__(16) float2 cs[TK][PAIRS];
   const int tok = threadIdx.x / PAIRS, i64 = threadIdx.x % PAIRS, c = i64 % V, h0 = i64 / V;
   const int n = blockIdx.x * TK + tok;
   const int H = n < a.N ? a.H[0] + a.H[1] : 0;
@@ -109,7 +109,11 @@ __global__ void __launch_bounds__(PAIRS * TK) rope_kernel(const __grid_constant_
   __syncthreads();
   float2 w[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) w[i] = cs[tok][c * E + i];
+  for (int i = 0; i < E; i += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(&cs[tok][c * E + i]);
+    w[i] = make_float2(v.x, v.y);
+    w[i + 1] = make_float2(v.z, v.w);
+  }
   for (int hb = h0; hb < H; hb += PRE * HS) {
 #pragma unroll
     for (int p = 0; p < PRE; ++p) {

@@ -63,8 +63,9 @@ def _int32(t: torch.Tensor, name: str, device: torch.device, dim: int = 1) -> to
 
 
 def _same_device(device: torch.device, *tensors: Optional[torch.Tensor]) -> None:
+    at = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != (-1 if at is None else at):
             raise ValueError(f"tensors on {t.device} and {device}")
 
 
@@ -309,13 +310,15 @@ def paged_decode_attn(params: Params, q: torch.Tensor, pool: Cache, table: torch
     """Attention of q [B, Hq, 128] over the pages table[b] (int32 [B, max_pages]) and the first seq_lens[b]
     tokens (int32 [B]) of each sequence, or the last `window` of them -> out [B, Hq, 128], or (out, lse)
     with return_lse (lse fp32 [B, Hq], natural log; -inf for an empty sequence).  tq_paged_decode_attn."""
-    if q.dim() != 3 or q.shape[-1] != 128 or not q.is_contiguous():
+    if q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [B, Hq, 128] tensor")
     B, Hq, _ = q.shape
     device = q.device
     _same_device(device, pool.k_codes, params.Pi, table, out, lse, workspace)
     _int32(seq_lens, "seq_lens", device)
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
+    rows, max_pages = table.shape if table.dim() == 2 else (-1, 0)
+    table_stride, step = table.stride() if table.dim() == 2 else (0, 0)
+    if table.dtype != torch.int32 or rows != B or (max_pages > 1 and step != 1):
         raise ValueError(f"table must be int32 [{B}, max_pages] with contiguous rows")
     if seq_lens.shape[0] != B:
         raise ValueError(f"seq_lens must have {B} entries")
@@ -336,7 +339,6 @@ def paged_decode_attn(params: Params, q: torch.Tensor, pool: Cache, table: torch
                                 device=device)
     _check(lib().tq_paged_decode_attn(
         ctypes.byref(p), q.data_ptr(), _dtype_code(q), B, Hq, ctypes.byref(c), table.data_ptr(),
-        table.stride(0) if B > 1 else max(table.stride(0), table.shape[1]), table.shape[1], seq_lens.data_ptr(),
-        int(window), float(scale), out.data_ptr(), _dtype_code(out), _ptr(lse), workspace.data_ptr(),
+        table_stride if B > 1 else max(table_stride, max_pages), max_pages, seq_lens.data_ptr(), window, scale, out.data_ptr(), _dtype_code(out), _ptr(lse), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _raw_stream(device)))
     return (out, lse) if return_lse else out
