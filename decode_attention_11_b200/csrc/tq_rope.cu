@@ -190,7 +190,7 @@ extern "C" tq_status tq_rope(const void* q, int64_t q_stride_n, int64_t q_stride
       return fail(TQ_ERR_INVALID_ARG, "q / k / outputs NULL or not 16-byte aligned");
     if (sn[w] < 0 || sh[w] < 0 || (sn[w] * es) % 16 || (sh[w] * es) % 16)
       return fail(TQ_ERR_INVALID_ARG, "strides (%lld, %lld) invalid", (long long)sn[w], (long long)sh[w]);
-    const bool packed = sh[w] == kHeadDim && sn[w] == (int64_t)H[w] * kHeadDim;
+    const bool packed = (H[w] == 1 || sh[w] == kHeadDim) && (N == 1 || sn[w] == (int64_t)H[w] * kHeadDim);
     if (x[w] == y[w] && !packed)
       return fail(TQ_ERR_INVALID_ARG, "in place needs a contiguous input");
   }

@@ -79,17 +79,20 @@ def _axes_of(sections: Tuple[int, ...]) -> bytes:
 
 
 def _rope_arg(x: Optional[torch.Tensor], out: Optional[torch.Tensor], name: str, N: int):
-    """((pointer, strides, heads) of x, its output)."""
+    """((pointer, strides, heads) of x, its output, the output's pointer)."""
     if x is None:
-        return (None, 0, 0, 0), None
-    if x.dim() != 3 or x.shape[0] != N or x.shape[2] != 128 or x.stride(2) != 1:
+        return (None, 0, 0, 0), None, None
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [N, H, 128]")
+    n, H, d = x.shape
+    sn, sh, sd = x.stride()
+    if n != N or d != 128 or sd != 1:
         raise ValueError(f"{name} must be [N, H, 128] with a contiguous last dim, N = {N}")
     if out is None:
-        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(N, x.shape[1], 128, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if sh == 128 and sn == 128 * H else torch.empty(N, H, 128, dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
         raise ValueError(f"{name}_out must be contiguous, of the shape and dtype of {name}")
-    sn, sh, _ = x.stride()
-    return (x.data_ptr(), sn, sh, x.shape[1]), out
+    return (x.data_ptr(), sn, sh, H), out, out.data_ptr()
 
 
 def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor, sections: Sequence[int] = (64,),
@@ -105,25 +108,31 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    device, N = x.device, x.shape[0]
-    if pos.dim() == 1:
-        pos = pos.unsqueeze(0)
-    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[1] != N or (N > 1 and pos.stride(1) != 1):
+    device, N, n_axes, pos_stride = x.device, x.shape[0], 1, 0
+    if pos.dim() == 2:
+        n_axes, n = pos.shape
+        pos_stride, step = pos.stride()
+    else:
+        n, step = (pos.shape[0], pos.stride(0)) if pos.dim() == 1 else (-1, 1)
+    if pos.dtype != torch.int32 or n != N or (N > 1 and step != 1):
         raise ValueError(f"pos must be int32 [axes, {N}] with contiguous rows")
-    _same_device(device, q, k, pos, q_out, k_out)
-    axes = bytes(axis_of_pair) if axis_of_pair is not None else _axes_of(tuple(sections))
-    if len(axes) != 64:
-        raise ValueError("axis_of_pair must have 64 entries")
+    if axis_of_pair is None:
+        axes = _axes_of(tuple(sections))
+    else:
+        axes = bytes(axis_of_pair)
+        if len(axes) != 64:
+            raise ValueError("axis_of_pair must have 64 entries")
     if q is not None and k is not None and q.dtype != k.dtype:
         raise ValueError("q and k must share their dtype")
     dt = _dtype_code(x)
+    _same_device(device, q, k, pos, q_out, k_out)
     if _elsewhere(device, stream):
         with _on(device, stream):
             return rope(q, k, pos, sections, base, style, inverse, axis_of_pair, q_out, k_out)
-    qa, q_out = _rope_arg(q, q_out, "q", N)
-    ka, k_out = _rope_arg(k, k_out, "k", N)
-    _check(lib().tq_rope(*qa, *ka, dt, N, pos.data_ptr(), pos.stride(0), pos.shape[0], axes, base, style, 1 if inverse else 0,
-                         _ptr(q_out), _ptr(k_out), _raw_stream(device)))
+    qa, q_out, qp = _rope_arg(q, q_out, "q", N)
+    ka, k_out, kp = _rope_arg(k, k_out, "k", N)
+    _check(lib().tq_rope(*qa, *ka, dt, N, pos.data_ptr(), pos_stride, n_axes, axes, base, style, 1 if inverse else 0, qp, kp,
+                         _raw_stream(device)))
     return q_out, k_out
 
 
@@ -339,6 +348,6 @@ def paged_decode_attn(params: Params, q: torch.Tensor, pool: Cache, table: torch
                                 device=device)
     _check(lib().tq_paged_decode_attn(
         ctypes.byref(p), q.data_ptr(), _dtype_code(q), B, Hq, ctypes.byref(c), table.data_ptr(),
-        table_stride if B > 1 else max(table_stride, max_pages), max_pages, seq_lens.data_ptr(), window, scale, out.data_ptr(), _dtype_code(out), _ptr(lse), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(device)))
+        table_stride if B > 1 else max(table_stride, max_pages), max_pages, seq_lens.data_ptr(), window, scale, out.data_ptr(),
+        _dtype_code(out), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(device)))
     return (out, lse) if return_lse else out

@@ -475,7 +475,8 @@ tq_status tq_paged_quantize(const tq_params* params, const void* k, const void* 
 /*
  * Read rows of a pool back as values, in the rotated basis (x ~= Pi^T xhat; scores against Pi q need
  * no rotation back):
- *   k_out, v_out  device [N, Hkv, 128] contiguous, of dtype: ||x|| / sqrt(128) * c[idx], rounded once
+ *   k_out, v_out  device [N, Hkv, 128] contiguous, 32-byte aligned, of dtype: ||x|| / sqrt(128) * c[idx],
+ *                 rounded once
  *   signs_out     device int8 [N, Hkv, 128]: +1 / -1 per sketch row, NULL to leave out
  *   rnorm_out     device float [N, Hkv]: ||r||, NULL to leave out
  *   slots         device int32 [N]; a slot outside the pool reads as zeros; repeats are allowed

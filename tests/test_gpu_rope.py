@@ -105,6 +105,14 @@ def test_rope_in_place_empty_and_graph():
     p = q.clone()
     r, _ = tq.rope(p, None, pos, q_out=p)
     assert r is p and torch.equal(p, want)
+    one = q[5:6]  # one token, one head: contiguous whatever the strides say
+    tq.rope(one, None, pos[5:6], q_out=one)
+    assert torch.equal(q[5], want[5])
+    q[5] = p.new_tensor(0)
+    lone = torch.randn(3, 9, 128, device="cuda")[1:2, 4:5]
+    keep = lone.clone()
+    tq.rope(lone, None, pos[7:8], q_out=lone)
+    assert torch.equal(lone, tq.rope(keep, None, pos[7:8])[0])
     e, _ = tq.rope(q[:0], None, pos[:0])
     assert e.shape == (0, H, 128)
     out = torch.empty_like(q)

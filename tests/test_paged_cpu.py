@@ -122,6 +122,7 @@ def test_row_calls_refuse():
         assert f(slots=None) == BAD and f(slots=FAKE + 2) == BAD and f(N=-1) == BAD and f(N=1 << 30) == BAD
         assert f(dtype=7) == UNSUPPORTED
         assert f(k=None) == BAD and f(v=FAKE + 8) == BAD
+    assert read(k=FAKE + 16) == BAD and read(v=FAKE + 16) == BAD
     assert quantize(sn=-256) == BAD and quantize(sh=4) == BAD and quantize(sn=257) == BAD
     assert quantize(N=0, k=None, v=None, slots=None) == tq.TQ_OK
     bare = pool(qjl_m=0, k_signs=None, k_rnorm=None)
