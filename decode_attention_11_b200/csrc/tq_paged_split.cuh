@@ -60,11 +60,16 @@ struct PLayout {
   // Pair tables: 4/4 bits: 256 entries of 256 bytes (key replicas at +0, value replicas at +128) at a
   // 64 KB boundary of the shared window, so that one byte permute makes an address of a byte of codes;
   // other widths: 128-byte entries, each table at a multiple of its size (the larger first), so that an
-  // address is a shifted field of codes or'ed into the lane's address of entry 0.
-  static constexpr bool kPacked = KB == 4 && VB == 4;
-  static constexpr int K_TBL = (1 << (2 * KB)) * 128, V_TBL = (1 << (2 * VB)) * 128;
+  // address is a shifted field of codes or'ed into the lane's address of entry 0.  2-bit values: entries of
+  // two pairs (two codes of each of two tokens: a byte) of 256 bytes at a 64 KB boundary, one 8-byte load
+  // for two operands.
+  static constexpr bool kPacked = KB == 4 && VB == 4, kQuadV = VB == 2;
+  static constexpr int K_TBL = (1 << (2 * KB)) * 128, V_TBL = kQuadV ? 65536 : (1 << (2 * VB)) * 128;
   static constexpr int TBL_BYTES = K_TBL + V_TBL;
-  static constexpr int TBL_ALIGN = kPacked ? 65536 : K_TBL > V_TBL ? K_TBL : V_TBL;
+  static constexpr int TBL_ALIGN = kPacked || kQuadV ? 65536 : K_TBL > V_TBL ? K_TBL : V_TBL;
+  // places of the tables
+  static constexpr uint32_t K_AT = kPacked || K_TBL >= V_TBL ? 0 : V_TBL;
+  static constexpr uint32_t V_AT = kPacked ? 128 : K_TBL >= V_TBL ? K_TBL : 0;
   // Rings of the warps, before the tables (the first 1 KB of the window is the system's) and behind them.
   static constexpr int FRONT = TBL_ALIGN > 1024 ? TBL_ALIGN - 1024 : 0;
   static constexpr int BACK = P_SMEM - P_MISC - TBL_BYTES - FRONT - 1024;
@@ -119,6 +124,11 @@ __device__ __forceinline__ uint32_t lut32(uint32_t p) {
   asm("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(p));
   return v;
 }
+__device__ __forceinline__ uint2 lut64(uint32_t p) {
+  uint2 v;
+  asm("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(p));
+  return v;
+}
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -157,7 +167,7 @@ __device__ __forceinline__ void v_codes_at(uint32_t p, uint32_t odd, uint32_t (&
     c[0] = ld32<OFF>(p);
   }
 }
-// Codes of two tokens a and b field by field: even fields to e, odd fields to o, each a | b << VB.
+// Codes of two tokens a and b field by field: even fields to e, odd fields to o, a's below b's.
 template <int VB, int NWORDS>
 __device__ __forceinline__ void interleave(const uint32_t (&a)[NWORDS], const uint32_t (&b)[NWORDS], uint32_t (&e)[NWORDS], uint32_t (&o)[NWORDS]) {
   auto sel = [](uint32_t m, uint32_t x, uint32_t y) { return (x & m) | (y & ~m); };
@@ -168,11 +178,11 @@ __device__ __forceinline__ void interleave(const uint32_t (&a)[NWORDS], const ui
     o[0] = sel((uint32_t)m, __funnelshift_r(a[0], a[1], 3), b[0]);
     o[1] = sel((uint32_t)(m >> 32), a[1] >> 3, b[1]);
   } else {
-    constexpr uint32_t m = VB == 4 ? 0x0F0F0F0Fu : 0x33333333u;
+    // (2-bit codes: fields of two codes, as the table of their quads wants them)
 #pragma unroll
     for (int i = 0; i < NWORDS; ++i) {
-      e[i] = sel(m, a[i], b[i] << VB);
-      o[i] = sel(m, a[i] >> VB, b[i]);
+      e[i] = sel(0x0F0F0F0Fu, a[i], b[i] << 4);
+      o[i] = sel(0x0F0F0F0Fu, a[i] >> 4, b[i]);
     }
   }
 }
@@ -234,21 +244,25 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
     if (lane == 0) pre[a.B] = sum;
   }
   // ---- pair tables: entry e = lo | hi << b -> half2(c[lo], c[hi]), a replica per lane, four to a store
-  constexpr uint32_t K_AT = Lay::kPacked || KB >= VB ? 0 : Lay::V_TBL;
-  constexpr uint32_t V_AT = Lay::kPacked ? 128 : KB >= VB ? Lay::K_TBL : 0;
   constexpr int PITCH = Lay::kPacked ? 256 : 128;
   unsigned char* tp = smem + (tbl - base);
   for (int i = tid; i < Lay::K_TBL / 16; i += Lay::THREADS) {
     const int e = i >> 3;
     const uint32_t v = pack_half2(cbs[e & ((1 << KB) - 1)], cbs[e >> KB]);
-    *reinterpret_cast<uint4*>(tp + K_AT + e * PITCH + 16 * (i & 7)) = make_uint4(v, v, v, v);
+    *reinterpret_cast<uint4*>(tp + Lay::K_AT + e * PITCH + 16 * (i & 7)) = make_uint4(v, v, v, v);
   }
   for (int i = tid; i < Lay::V_TBL / 16; i += Lay::THREADS) {
-    const int e = i >> 3;
-    const uint32_t v = pack_half2(cbs[16 + (e & ((1 << VB) - 1))], cbs[16 + (e >> VB)]);
-    *reinterpret_cast<uint4*>(tp + V_AT + e * PITCH + 16 * (i & 7)) = make_uint4(v, v, v, v);
+    if constexpr (Lay::kQuadV) {  // entry: two codes of token a (low four bits), two of token b
+      const int e = i >> 4, a4 = e & 15, b4 = e >> 4;
+      const uint32_t v = pack_half2(cbs[16 + (a4 & 3)], cbs[16 + (b4 & 3)]), w = pack_half2(cbs[16 + (a4 >> 2)], cbs[16 + (b4 >> 2)]);
+      *reinterpret_cast<uint4*>(tp + Lay::V_AT + 16 * i) = make_uint4(v, w, v, w);
+    } else {
+      const int e = i >> 3;
+      const uint32_t v = pack_half2(cbs[16 + (e & ((1 << VB) - 1))], cbs[16 + (e >> VB)]);
+      *reinterpret_cast<uint4*>(tp + Lay::V_AT + e * PITCH + 16 * (i & 7)) = make_uint4(v, v, v, v);
+    }
   }
-  const uint32_t rk = (tbl + K_AT) | (4u * lane), rv = (tbl + V_AT) | (4u * lane);
+  const uint32_t rk = (tbl + Lay::K_AT) | (4u * lane), rv = (tbl + Lay::V_AT) | ((Lay::kQuadV ? 8u : 4u) * lane);
   __syncthreads();
   // a batch too large for shared memory: the prep kernel's sums
   if (!few) asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -570,12 +584,20 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
         v_codes_at<VB, 8 * Lay::V_ROW>(vq, v_odd, y);
         interleave<VB>(x, y, e89, o89);
       }
+      // (2-bit values: a byte of e or o holds blocks 2j or 2j + 1 of both tokens)
 #define TQ_STEP(DB)                                                                                   \
       {                                                                                               \
-        const uint32_t A[4] = {pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(e01, rv),                  \
-                               pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(o01, rv),                  \
-                               pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(e89, rv),                  \
-                               pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(o89, rv)};                 \
+        uint32_t A[4];                                                                                \
+        if constexpr (Lay::kQuadV) {                                                                  \
+          const uint2 x = lut64(__byte_perm(((DB) & 1 ? o01 : e01)[0], rv, 0x7604u | (((DB) / 2) << 4)));  \
+          const uint2 y = lut64(__byte_perm(((DB) & 1 ? o89 : e89)[0], rv, 0x7604u | (((DB) / 2) << 4)));  \
+          A[0] = x.x; A[1] = x.y; A[2] = y.x; A[3] = y.y;                                             \
+        } else {                                                                                      \
+          A[0] = pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(e01, rv);                                \
+          A[1] = pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(o01, rv);                                \
+          A[2] = pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(e89, rv);                                \
+          A[3] = pair_of<Lay::kPacked, 2 * VB * (DB), 2 * VB>(o89, rv);                                \
+        }                                                                                             \
         _Pragma("unroll") for (int nb = 0; nb < NB; ++nb) mma(oacc[DB], A, bp[nb]);                    \
       }
       TQ_STEP(0) TQ_STEP(1) TQ_STEP(2) TQ_STEP(3) TQ_STEP(4) TQ_STEP(5) TQ_STEP(6) TQ_STEP(7)
