@@ -26,36 +26,60 @@ __device__ unsigned int g_paged_error;
 
 // -------------------------------------------------------------------------- 128 x 128 products
 //
-// Prep and merge multiply Pi, S and Pi^T with the vectors of up to eight heads.  On the FP32 units such
-// a product is bound by reading the vectors from shared memory (16 us for 512 units of eight heads);
-// here warp w keeps rows 16w .. 16w + 15 of the matrix as m16n8k16 A fragments, fp16 hi + lo of 2^8 M,
-// for all units it meets, and the heads are the 8 columns.  The vectors enter as fp16 hi + lo of x 2^e
-// with max |x| 2^e in [2^10, 2^11): M x = 2^-(8+e) (Mhi xhi + Mhi xlo + Mlo xhi), off by about 2^-22.
+// Prep and merge multiply Pi, S and Pi^T with the vectors of many heads.  On the FP32 units such a
+// product is bound by reading the vectors from shared memory (32 us for 512 units of eight heads in
+// prep); here warp w keeps rows 16w .. 16w + 15 of the matrix as m16n8k16 A fragments, fp16 hi + lo of
+// 2^8 M, for all heads it meets, and a CTA takes 8 or 16 heads at a time as the columns.  The vectors
+// enter as fp16 hi + lo of x 2^e with max |x| 2^e in [2^10, 2^11), converted once and shared:
+// M x = 2^-(8+e) (Mhi xhi + Mhi xlo + Mlo xhi), off by about 2^-22.
+// The order of the columns in a k-step is free: k-step kk of lane t is columns 16kk + 4t .. + 3.
 
 constexpr int MT = 256;              // threads: eight warps of 16 rows
-constexpr int VS = D + 4;            // stride of a head's vector in shared memory (no bank conflicts)
+constexpr int MW = MT / 32;
 constexpr float M_SCALE = 256.0f;
+
+// x and y as pairs of fp16 hi and lo parts.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
 
 template <bool LO>
 struct AFrag {
   uint32_t hi[8][4], lo[LO ? 8 : 1][4];
   __device__ __forceinline__ void set(int kk, int r, float x, float y) {
-    x *= M_SCALE;
-    y *= M_SCALE;
-    float xh, xl, yh, yl;
-    split_half(x, xh, xl);
-    split_half(y, yh, yl);
-    hi[kk][r] = pack_half2(xh, yh);
-    if constexpr (LO) lo[kk][r] = pack_half2(xl, yl);
+    uint32_t l;
+    split_pair(x * M_SCALE, y * M_SCALE, hi[kk][r], l);
+    if constexpr (LO) lo[kk][r] = l;
   }
-  // rows 16w + gq (+ 8) of a row-major matrix, columns 16kk + 2t (+ 8), + 1
+  // as laid out by store(): 16 KB of a warp's fragments in 16-byte words
+  __device__ __forceinline__ void store(uint4* w, int lane) const {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      w[64 * kk + lane] = make_uint4(hi[kk][0], hi[kk][1], hi[kk][2], hi[kk][3]);
+      w[64 * kk + 32 + lane] = make_uint4(lo[kk][0], lo[kk][1], lo[kk][2], lo[kk][3]);
+    }
+  }
+  __device__ __forceinline__ void fetch(const uint4* w, int lane) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      const uint4 h = __ldcg(w + 64 * kk + lane), l = __ldcg(w + 64 * kk + 32 + lane);
+      hi[kk][0] = h.x; hi[kk][1] = h.y; hi[kk][2] = h.z; hi[kk][3] = h.w;
+      lo[kk][0] = l.x; lo[kk][1] = l.y; lo[kk][2] = l.z; lo[kk][3] = l.w;
+    }
+  }
+  // rows 16w + gq (+ 8) of a row-major matrix
   __device__ __forceinline__ void load(const float* M, int w, int gq, int t) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(M + (16 * w + gq + 8 * (r & 1)) * D + 16 * kk + 2 * t + 8 * (r >> 1)));
+      for (int r = 0; r < 2; ++r) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(M + (16 * w + gq + 8 * r) * D + 16 * kk + 4 * t));
         set(kk, r, v.x, v.y);
+        set(kk, 2 + r, v.z, v.w);
       }
   }
   // the same of its transpose
@@ -64,62 +88,92 @@ struct AFrag {
     for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float* m = M + (16 * kk + 2 * t + 8 * (r >> 1)) * D + 16 * w + gq + 8 * (r & 1);
+        const float* m = M + (16 * kk + 4 * t + 2 * (r >> 1)) * D + 16 * w + gq + 8 * (r & 1);
         set(kk, r, __ldg(m), __ldg(m + D));
       }
   }
 };
 
-// A lane's share of its column's vector: x[4kk + 2r + i] = element 16kk + 8r + 2t + i of head gq.
-// Products of the warp's 16 rows with the eight vectors: y[0], y[1]: row gq of heads 2t, 2t + 1, y[2],
-// y[3]: row gq + 8.
-template <bool LO>
-__device__ __forceinline__ void rows_times(const AFrag<LO>& A, const float (&x)[32], float (&y)[4]) {
-  float mx = 0.0f;
+// Vectors of R heads as B operands: fp16 pairs of columns 2j, 2j + 1, hi and lo parts, and the factor
+// 2^-(8+e) of each.
+template <int R>
+struct Vecs {
+  static constexpr int W = D / 2 + 4;  // words of a row (no bank conflicts)
+  uint32_t hi[R][W], lo[R][W];
+  float down[R];
+  // by one warp: row r, lane l holding elements 4l .. 4l + 3
+  __device__ __forceinline__ void put(int r, int lane, const float4& v) {
+    float mx = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-  for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
-  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-  int e = ((__float_as_int(mx) >> 23) & 255) - 127;
-  e = e < -100 ? -100 : e > 126 ? 126 : e;  // (infinities and NaN stay what they are)
-  const float up = __int_as_float((127 + 10 - e) << 23);
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+    int e = ((__float_as_int(mx) >> 23) & 255) - 127;
+    e = e < -100 ? -100 : e > 126 ? 126 : e;  // (infinities and NaN stay what they are)
+    const float up = __int_as_float((127 + 10 - e) << 23);
+    uint2 h, l;
+    split_pair(v.x * up, v.y * up, h.x, l.x);
+    split_pair(v.z * up, v.w * up, h.y, l.y);
+    *reinterpret_cast<uint2*>(&hi[r][2 * lane]) = h;
+    *reinterpret_cast<uint2*>(&lo[r][2 * lane]) = l;
+    if (lane == 0) down[r] = __int_as_float((127 + e - 18) << 23);  // 2^(e - 10) / 2^8
+  }
+};
+
+// Products of a warp's 16 matrix rows with vectors 8 nb .. 8 nb + 7: y[0], y[1]: row gq of vectors
+// 8 nb + 2t, + 1; y[2], y[3]: row gq + 8.
+template <bool LO, int R>
+__device__ __forceinline__ void rows_times(const AFrag<LO>& A, const Vecs<R>& x, int nb, int gq, int t, float (&y)[4]) {
   float d[2][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) d[0][i] = d[1][i] = 0.0f;
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {
-    uint32_t bh[2], bl[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float h0, l0, h1, l1;
-      split_half(x[4 * kk + 2 * r] * up, h0, l0);
-      split_half(x[4 * kk + 2 * r + 1] * up, h1, l1);
-      bh[r] = pack_half2(h0, h1);
-      bl[r] = pack_half2(l0, l1);
-    }
-    mma16816(d[0], A.hi[kk], bh[0], bh[1]);
-    mma16816(d[1], A.hi[kk], bl[0], bl[1]);
-    if constexpr (LO) mma16816(d[1], A.lo[kk], bh[0], bh[1]);
+    const uint2 bh = *reinterpret_cast<const uint2*>(&x.hi[8 * nb + gq][8 * kk + 2 * t]);
+    const uint2 bl = *reinterpret_cast<const uint2*>(&x.lo[8 * nb + gq][8 * kk + 2 * t]);
+    mma16816(d[0], A.hi[kk], bh.x, bh.y);
+    mma16816(d[1], A.hi[kk], bl.x, bl.y);
+    if constexpr (LO) mma16816(d[1], A.lo[kk], bh.x, bh.y);
   }
-  const float down = __int_as_float((127 + e - 18) << 23);  // of head gq: 2^(e - 10) / 2^8
-  const int t = threadIdx.x & 3;
-  const float d0 = __shfl_sync(FULL, down, 8 * t), d1 = __shfl_sync(FULL, down, 8 * t + 4);
+  const float d0 = x.down[8 * nb + 2 * t], d1 = x.down[8 * nb + 2 * t + 1];
   y[0] = (d[0][0] + d[1][0]) * d0;
   y[1] = (d[0][1] + d[1][1]) * d1;
   y[2] = (d[0][2] + d[1][2]) * d0;
   y[3] = (d[0][3] + d[1][3]) * d1;
 }
-__device__ __forceinline__ void lane_share(const float* v, float (&x)[32]) {  // v: the head's vector
-  const int t = threadIdx.x & 3;
+// ... of all R vectors, to rows of fp32 results.
+constexpr int VS = D + 4;
+template <bool LO, int R>
+__device__ __forceinline__ void product(const AFrag<LO>& A, const Vecs<R>& x, float (*res)[VS], int warp, int gq, int t) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 p = *reinterpret_cast<const float2*>(v + 8 * i + 2 * t);
-    x[2 * i] = p.x;
-    x[2 * i + 1] = p.y;
+  for (int nb = 0; nb < R / 8; ++nb) {
+    float y[4];
+    rows_times(A, x, nb, gq, t, y);
+    const int row = 16 * warp + gq;
+    res[8 * nb + 2 * t][row] = y[0];
+    res[8 * nb + 2 * t + 1][row] = y[1];
+    res[8 * nb + 2 * t][row + 8] = y[2];
+    res[8 * nb + 2 * t + 1][row + 8] = y[3];
   }
 }
 
+// Heads are numbered with the gaps of units that are not full: head p is column p % hgn of unit p / hgn.
+struct HeadPlace {
+  int unit, col;
+  bool live;
+  int64_t row;  // of q and out: b Hq + h
+};
+__device__ __forceinline__ HeadPlace head_place(int p, int hgn, int hgroups, int g, int units) {  // (p < 2^25)
+  HeadPlace h;
+  h.unit = p >> (hgn == 4 ? 2 : 3);
+  h.col = p - h.unit * hgn;
+  const int bk = h.unit / hgroups, hg = h.unit - bk * hgroups;
+  h.live = h.unit < units && h.col < min(HG, g - hg * HG);
+  h.row = (int64_t)bk * g + hg * HG + h.col;
+  return h;
+}
+
 // ------------------------------------------------------------------------------------------ prep
+
+constexpr int PR = 16;  // heads of a CTA at a time, two per warp
 
 struct PrepArgs {
   int B, Hq, Hkv, g, hgroups, nb;
@@ -132,18 +186,27 @@ struct PrepArgs {
   const int32_t* lens;
   uint32_t* ops;
   int64_t* before;
+  uint4* pit;  // fragments of Pi^T, for the merge kernel
   unsigned int* err;
 };
 
 template <bool QJL>
 __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ PrepArgs a) {
-  __shared__ float qs[HG][VS], ss[HG][VS];
-  __shared__ float4 hc[HG];
-  __shared__ int64_t wsum[MT / 32];
+  __shared__ __align__(16) Vecs<PR> vec;
+  __shared__ __align__(16) float qs[PR][VS];
+  __shared__ __align__(16) float ss[QJL ? PR : 1][VS];
+  __shared__ __align__(16) uint32_t tile[PR * seg_bytes(1) / 16];  // operands of the heads' units
+  __shared__ int64_t wsum[MW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if (blockIdx.x == gridDim.x - 1) {
-    // the last CTA: groups of the sequences before each one
+    // the last CTA: the fragments of Pi^T (a CTA of the merge kernel that formed them itself spent half its
+    // time on it), and the groups of the sequences before each one
+    {
+      AFrag<true> pt;
+      pt.load_t(a.Pi, warp, lane >> 2, lane & 3);
+      pt.store(a.pit + 512 * warp, lane);
+    }
     if (tid == 0) *a.err = 0u;
     int64_t base = 0;
     bool bad = false;
@@ -162,7 +225,7 @@ __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ Prep
       if (lane == 31) wsum[warp] = x;
       __syncthreads();
       int64_t low = 0, all = 0;
-      for (int w = 0; w < MT / 32; ++w) {
+      for (int w = 0; w < MW; ++w) {
         low += w < warp ? wsum[w] : 0;
         all += wsum[w];
       }
@@ -174,249 +237,269 @@ __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ Prep
     return;
   }
   const int gq = lane >> 2, t = lane & 3, hgn = 4 * a.nb, ctas = gridDim.x - 1;
-  const int seg_words = seg_bytes(a.nb) / 4;
-  // this lane's share of head gq of unit u (0 past the unit's heads)
-  auto load_q = [&](int u, float (&x)[32]) {
-    const int hg = u % a.hgroups, bk = u / a.hgroups;
-    const bool live = u < a.units && gq < min(HG, a.g - hg * HG);
-    const int64_t at = ((int64_t)bk * a.g + hg * HG + gq) * D + 2 * t;
-    if (!live) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = 0.0f;
-    } else if (a.q_bf16) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + at + 8 * i));
-        x[2 * i] = __uint_as_float(w << 16);
-        x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 w = __ldg(reinterpret_cast<const float2*>(reinterpret_cast<const float*>(a.q) + at + 8 * i));
-        x[2 * i] = w.x;
-        x[2 * i + 1] = w.y;
-      }
-    }
+  const int heads = a.units * hgn;
+  auto load_q = [&](int p) -> float4 {
+    const HeadPlace h = head_place(p, hgn, a.hgroups, a.g, a.units);
+    if (!h.live) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (!a.q_bf16) return __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + h.row * D) + lane);
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) + h.row * D) + lane);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
   };
-  float next[32];
-  load_q(blockIdx.x, next);
+  float4 next[2];
+  next[0] = load_q(blockIdx.x * PR + 2 * warp);
+  next[1] = load_q(blockIdx.x * PR + 2 * warp + 1);
   AFrag<true> pi;
   AFrag<false> sk;
   pi.load(a.Pi, warp, gq, t);
   if constexpr (QJL) sk.load(a.S, warp, gq, t);  // (entries exact in fp16)
-  for (int u = blockIdx.x; u < a.units; u += ctas) {
-    const int hg = u % a.hgroups, nh = min(HG, a.g - hg * HG);
-    float x[32], y[4];
+  for (int p0 = blockIdx.x * PR; p0 < heads; p0 += ctas * PR) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = next[i];
-    load_q(u + ctas, next);
-    rows_times(pi, x, y);
-    const int row = 16 * warp + gq;
-    qs[2 * t][row] = y[0];
-    qs[2 * t + 1][row] = y[1];
-    qs[2 * t][row + 8] = y[2];
-    qs[2 * t + 1][row + 8] = y[3];
+    for (int x = 0; x < 2; ++x) {
+      vec.put(2 * warp + x, lane, next[x]);
+      next[x] = load_q(p0 + ctas * PR + 2 * warp + x);
+    }
     __syncthreads();
+    product(pi, vec, qs, warp, gq, t);
+    __syncthreads();
+    float4 q4[2], s4[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      q4[x] = *reinterpret_cast<const float4*>(&qs[2 * warp + x][4 * lane]);
+      s4[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     if constexpr (QJL) {
-      lane_share(qs[gq], x);
-      rows_times(sk, x, y);
-      ss[2 * t][row] = y[0];
-      ss[2 * t + 1][row] = y[1];
-      ss[2 * t][row + 8] = y[2];
-      ss[2 * t + 1][row + 8] = y[3];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) vec.put(2 * warp + x, lane, q4[x]);
       __syncthreads();
+      product(sk, vec, ss, warp, gq, t);
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) s4[x] = *reinterpret_cast<const float4*>(&ss[2 * warp + x][4 * lane]);
     }
-    // per head: a power of two 2^-e that brings q' and 16 S q' below 2^14 (fp16 range), and the QJL
+    // Per head: a power of two 2^-e that brings q' and 16 S q' below 2^14 (fp16 range), and the QJL
     // constant Kh = -C - 0.5 sum_l sq_l 2^-e, C the sum of the fp16 parts of the pre-scaled S q':
-    // sum_l sq_l (2 b_l - 1) = 2 (D_hi + D_lo + Kh) in the split kernel's product
-    if (warp < hgn) {
-      const int h = warp;
-      if (h >= nh) {
-        if (lane == 0) hc[h] = make_float4(a.sK, a.sQ, 0.0f, 1.0f);
-      } else {
-        float mx = 0.0f;
+    // sum_l sq_l (2 b_l - 1) = 2 (D_hi + D_lo + Kh) in the split kernel's product.
+    // Then the head's fragments: k-step kk holds k = 16kk + 2t, + 1 (register 0), + 8, + 9 (register 1)
+    // of lane (gq, t); word 2kk + r of a lane is q', word 16 + 2kk + r is S q'; a unit's words are
+    // [block][word / 4][lane][word % 4] with columns as seg_bytes says.
 #pragma unroll
-        for (int k = lane; k < D; k += 32) mx = fmaxf(mx, fmaxf(fabsf(qs[h][k]), QJL ? 16.0f * fabsf(ss[h][k]) : 0.0f));
+    for (int x = 0; x < 2; ++x) {
+      const HeadPlace h = head_place(p0 + 2 * warp + x, hgn, a.hgroups, a.g, a.units);
+      const float qv[4] = {q4[x].x, q4[x].y, q4[x].z, q4[x].w}, sv[4] = {s4[x].x, s4[x].y, s4[x].z, s4[x].w};
+      float mx = 0.0f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-        const int ex = (mx < 16384.0f || !(mx < INFINITY)) ? 0 : ((__float_as_int(mx) >> 23) & 255) - 127 - 13;
-        const float dn = __int_as_float((127 - ex) << 23);
-        float ch = 0.0f, sh = 0.0f;
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(qv[i]), 16.0f * fabsf(sv[i])));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+      const int ex = (mx < 16384.0f || !(mx < INFINITY)) ? 0 : ((__float_as_int(mx) >> 23) & 255) - 127 - 13;
+      const float dn = __int_as_float((127 - ex) << 23);
+      const float scl = (float)(16 >> ((lane >> 1) & 3));  // sgn_scale of the lane's k-step pair
+      uint32_t qh[2], ql[2], sh[2], sl[2];
+      float ch = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        split_pair(qv[2 * i] * dn, qv[2 * i + 1] * dn, qh[i], ql[i]);
+        split_pair(sv[2 * i] * dn * scl, sv[2 * i + 1] * dn * scl, sh[i], sl[i]);
+        const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&sh[i])), fl = __half22float2(*reinterpret_cast<const __half2*>(&sl[i]));
+        ch += (fh.x + fl.x) + (fh.y + fl.y);
+      }
+      float sum = ch * (1.0f / scl);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        ch += __shfl_xor_sync(FULL, ch, o);
+        sum += __shfl_xor_sync(FULL, sum, o);
+      }
+      // this head's unit in the tile
+      uint32_t* u = tile + (2 * warp + x) / hgn * (seg_bytes(a.nb) / 4);
+      const int word = 2 * (lane >> 2) + ((lane & 3) >> 1), t0 = 2 * (lane & 1);
+      const int ln = a.nb == 1 ? 8 * h.col : 4 * h.col;                      // lane 4 gq of the hi column
+      const int lo = a.nb == 1 ? 16 : 1024;                                  // words from hi to lo
+      uint32_t* w = u + (word >> 2) * 128 + (ln + t0) * 4 + (word & 3);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[4 * i] = qh[i];
+        w[lo + 4 * i] = ql[i];
         if constexpr (QJL) {
-#pragma unroll
-          for (int k = lane; k < D; k += 32) {
-            const float scl = (float)(16 >> ((k >> 3) & 3));  // sgn_scale of the k-step pair
-            const float v = ss[h][k] * dn * scl;
-            const float hi = __half2float(__float2half_rn(v));
-            const float lo = __half2float(__float2half_rn(v - hi));
-            ch += hi + lo;
-            sh += (hi + lo) * (1.0f / scl);
-          }
-#pragma unroll
-          for (int o = 16; o; o >>= 1) {
-            ch += __shfl_xor_sync(FULL, ch, o);
-            sh += __shfl_xor_sync(FULL, sh, o);
-          }
+          w[512 + 4 * i] = sh[i];
+          w[512 + lo + 4 * i] = sl[i];
         }
-        if (lane == 0) {
-          const float up = __int_as_float((127 + ex) << 23);
-          hc[h] = make_float4(a.sK * up, a.sQ * up, -ch - 0.5f * sh, dn);
-        }
+      }
+      if (lane == 0) {
+        const float up = __int_as_float((127 + ex) << 23);
+        reinterpret_cast<float4*>(u + a.nb * 1024)[h.col] = make_float4(a.sK * up, a.sQ * up, -ch - 0.5f * sum, dn);
       }
     }
     __syncthreads();
-    // Fragments: columns as seg_bytes says; k-step kk holds k = 16kk + 2t, + 1 (register 0), + 8, + 9
-    // (register 1) of lane (gq, t).  Word 2kk + r of a lane is q', word 16 + 2kk + r is S q'; stored
-    // [block][word / 4][lane][word % 4].
-    uint4* dst = reinterpret_cast<uint4*>(a.ops + (int64_t)u * seg_words);
-    for (int i = tid; i < a.nb * 256; i += MT) {
-      const int w4 = (i >> 5) & 7, ln = i & 31, nb = i >> 8, sq = w4 >> 2;
-      const int h = a.nb == 1 ? ln >> 3 : ln >> 2;
-      const bool lo = a.nb == 1 ? (ln >> 2) & 1 : nb;
-      uint32_t v[4] = {0u, 0u, 0u, 0u};
-      if (h < nh && (!sq || QJL)) {
-        const float* src = (sq ? ss[h] : qs[h]) + 32 * (w4 & 3) + 2 * (ln & 3);
-        const float dn = hc[h].w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // k-steps 2 (w4 % 4) and + 1, both registers
-          const float f = dn * (sq ? sgn_scale(j) : 1.0f);
-          float h0, l0, h1, l1;
-          split_half(src[8 * j] * f, h0, l0);
-          split_half(src[8 * j + 1] * f, h1, l1);
-          v[j] = lo ? pack_half2(l0, l1) : pack_half2(h0, h1);
-        }
-      }
-      dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
-    }
-    if (tid < hgn) reinterpret_cast<float4*>(dst + a.nb * 256)[tid] = hc[tid];
-    __syncthreads();  // the next unit reuses the vectors
+    const int u0 = p0 / hgn, n = min(PR / hgn, a.units - u0) * (seg_bytes(a.nb) / 16);
+    uint4* dst = reinterpret_cast<uint4*>(a.ops + (int64_t)u0 * (seg_bytes(a.nb) / 4));
+    for (int i = tid; i < n; i += MT) dst[i] = reinterpret_cast<const uint4*>(tile)[i];
+    // (the tile is written again behind the next round's barriers)
   }
 }
 
 // ------------------------------------------------------------------------------------------ merge
 //
-// A CTA joins the partials of all heads of a unit (warp h those of head h) or, when there are too few
-// units to fill the SMs, of one head (the warps share its partials), and turns the joined o' back:
-// o_i = sum_j Pi[j][i] o'_j, with Pi^T loaded before the wait for the split kernel.
-
-constexpr int MW = MT / 32;
+// HPW heads per warp: a CTA joins the partials of 8 HPW heads and turns the joined o' back,
+// o_i = sum_j Pi[j][i] o'_j.  HPW = 0, for too few
+// heads to fill the SMs: one head, whose partials the eight warps share.
 
 struct MergeArgs {
-  int B, Hq, Hkv, g, hgroups, hgn, ctas, warps, items;
+  int B, Hq, Hkv, g, hgroups, hgn, ctas, warps, units;
   const float* part;
   const int64_t* before;
-  const float* Pi;
+  const uint4* pit;
   const unsigned int* err;
   void* out;
   int out_bf16;
   float* lse;
 };
 
-template <bool ONE>
+// Partials of a unit: its own record (of the warp, or the joint CTA, that opens it), then those of the
+// warps that go on with it: in the CTA where the unit opens, one for each CTA inside the unit, and in the
+// CTA where it ends (one if that CTA ends with it).
+struct Records {
+  int S, w0, c0, c1, in0, mid, warps;
+  int64_t unit, units;
+  __device__ __forceinline__ void of(int64_t N, const Cut& cut, int64_t f0, int64_t G, int64_t u, int64_t all) {
+    unit = u;
+    units = all;
+    warps = cut.warps;
+    S = w0 = c0 = c1 = in0 = mid = 0;
+    if (G == 0) return;
+    const int64_t f1 = f0 + G;
+    w0 = range_of(N, cut, f0);
+    const int w1 = range_of(N, cut, f1 - 1);
+    c0 = w0 / warps;
+    c1 = w1 / warps;
+    const bool joint0 = range_start(N, cut, (int64_t)c0 * warps) == f0 && range_start(N, cut, (int64_t)(c0 + 1) * warps) <= f1;
+    in0 = joint0 ? 0 : min(w1, (c0 + 1) * warps - 1) - w0;
+    mid = max(0, c1 - c0 - 1);
+    S = 1 + in0 + mid;
+    if (c1 > c0) S += range_start(N, cut, (int64_t)(c1 + 1) * warps) == f1 ? 1 : w1 - c1 * warps + 1;
+  }
+  __device__ __forceinline__ int64_t slot(int s) const {
+    if (s == 0) return unit;
+    return units + (s <= in0 ? w0 + s : s <= in0 + mid ? (c0 + s - in0) * warps : c1 * warps + s - 1 - in0 - mid);
+  }
+};
+
+template <int HPW>
 __global__ void __launch_bounds__(MT) paged_merge(const __grid_constant__ MergeArgs a) {
-  __shared__ float os[HG][VS];              // joined o' of each head
-  __shared__ float rm[MW], rl[MW], ro[ONE ? MW : 1][D];
+  constexpr bool ONE = HPW == 0;
+  constexpr int R = ONE ? 8 : 8 * HPW;
+  __shared__ __align__(16) Vecs<R> vec;
+  __shared__ __align__(16) float res[R][VS];
+  __shared__ float rm[MW], rl[MW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, t = lane & 3;
-  AFrag<true> pt;
-  pt.load_t(a.Pi, warp, gq, t);
-  for (int i = tid; i < HG * VS; i += MT) (&os[0][0])[i] = 0.0f;  // columns without a head
-  __syncthreads();
+  vec.put(warp, lane, make_float4(0.0f, 0.0f, 0.0f, 0.0f));  // (ONE: the columns without a head)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  AFrag<true> pt;
+  pt.fetch(a.pit + 512 * warp, lane);
   if (blockIdx.x == 0 && tid == 0 && *a.err) atomicOr(&g_paged_error, *a.err);
   const int U = a.Hkv * a.hgroups;
   const int64_t N = __ldcg(a.before + a.B) * U;
   const Cut cut = cut_of(N, a.ctas, a.warps);
-  for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int u = ONE ? item / a.hgn : item, h0 = ONE ? item % a.hgn : 0;
-    const int b = u / U, uu = u - b * U, hg = uu % a.hgroups, kvh = uu / a.hgroups;
-    const int nh = min(HG, a.g - hg * HG);
-    if (ONE && h0 >= nh) continue;
-    const int64_t orow = (int64_t)b * a.Hq + (int64_t)kvh * a.g + hg * HG;
-    const int64_t lo = __ldcg(a.before + b), G = __ldcg(a.before + b + 1) - lo;
-    // Partials: the unit's own record (of the warp, or the joint CTA, that opens it), then those of the
-    // warps that go on with it: in the CTA where the unit opens, one for each CTA inside the unit, and in
-    // the CTA where it ends (one if that CTA ends with it).
-    int S = 0, w0 = 0, c0 = 0, c1 = 0, in0 = 0, mid = 0;
-    if (G > 0) {
-      const int64_t f0 = lo * U + (int64_t)uu * G, f1 = f0 + G;
-      w0 = range_of(N, cut, f0);
-      const int w1 = range_of(N, cut, f1 - 1);
-      c0 = w0 / cut.warps;
-      c1 = w1 / cut.warps;
-      const bool joint0 = range_start(N, cut, (int64_t)c0 * cut.warps) == f0 && range_start(N, cut, (int64_t)(c0 + 1) * cut.warps) <= f1;
-      in0 = joint0 ? 0 : min(w1, (c0 + 1) * cut.warps - 1) - w0;
-      mid = max(0, c1 - c0 - 1);
-      S = 1 + in0 + mid;
-      if (c1 > c0) S += range_start(N, cut, (int64_t)(c1 + 1) * cut.warps) == f1 ? 1 : w1 - c1 * cut.warps + 1;
-    }
-    auto slot_of = [&](int s) -> int64_t {
-      if (s == 0) return u;
-      const int W = s <= in0 ? w0 + s : s <= in0 + mid ? (c0 + s - in0) * cut.warps : c1 * cut.warps + s - 1 - in0 - mid;
-      return (int64_t)a.B * U + W;
-    };
-    const int h = ONE ? h0 : warp;
-    float M = -1e30f, L = 0.0f;
-    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (h < nh) {
-#pragma unroll 4
-      for (int s = ONE ? warp : 0; s < S; s += ONE ? MW : 1) {
-        const float* p = a.part + (slot_of(s) * a.hgn + h) * PART;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p));
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
-        const float Mn = fmaxf(M, ml.x);
-        const float w0 = ex2(M - Mn), w1 = ex2(ml.x - Mn);
-        L = fmaf(w1, ml.y, L * w0);
-        O.x = fmaf(w1, o.x, O.x * w0);
-        O.y = fmaf(w1, o.y, O.y * w0);
-        O.z = fmaf(w1, o.z, O.z * w0);
-        O.w = fmaf(w1, o.w, O.w * w0);
-        M = Mn;
-      }
-    }
-    if constexpr (ONE) {
-      if (lane == 0) {
-        rm[warp] = M;
-        rl[warp] = L;
-      }
-      *reinterpret_cast<float4*>(&ro[warp][4 * lane]) = O;
-      __syncthreads();
-      if (warp == 0) {
-        O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        L = 0.0f;
+  const int heads = a.units * a.hgn;
+  constexpr int STEP = ONE ? 1 : R;
+  for (int p0 = blockIdx.x * STEP; p0 < heads; p0 += gridDim.x * STEP) {
+    if (ONE && !head_place(p0, a.hgn, a.hgroups, a.g, a.units).live) continue;
 #pragma unroll
-        for (int k = 0; k < MW; ++k) M = fmaxf(M, rm[k]);
+    for (int x = 0; x < (ONE ? 1 : HPW); ++x) {
+      const HeadPlace h = head_place(ONE ? p0 : p0 + HPW * warp + x, a.hgn, a.hgroups, a.g, a.units);
+      float M = -1e30f, L = 0.0f;
+      float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      int S = 0;
+      if (h.live) {
+        const int b = h.unit / U, uu = h.unit - b * U;
+        const int64_t lo = __ldcg(a.before + b), G = __ldcg(a.before + b + 1) - lo;
+        Records rec;
+        rec.of(N, cut, lo * U + (int64_t)uu * G, G, h.unit, a.units);
+        S = rec.S;
+        constexpr int BATCH = 4, NEXT = ONE ? MW : 1;  // (loads of a batch together: one at a time they
+        for (int s0 = ONE ? warp : 0; s0 < S; s0 += BATCH * NEXT) {  // took 9 us for a unit of 17 partials)
+          float2 ml[BATCH];
+          float4 o[BATCH];
 #pragma unroll
-        for (int k = 0; k < MW; ++k) {
-          const float w = ex2(rm[k] - M);
-          const float4 o = *reinterpret_cast<const float4*>(&ro[k][4 * lane]);
-          L = fmaf(w, rl[k], L);
-          O.x = fmaf(w, o.x, O.x);
-          O.y = fmaf(w, o.y, O.y);
-          O.z = fmaf(w, o.z, O.z);
-          O.w = fmaf(w, o.w, O.w);
+          for (int i = 0; i < BATCH; ++i) {
+            const int s = s0 + i * NEXT;
+            const float* p = a.part + (rec.slot(s < S ? s : 0) * a.hgn + h.col) * PART;
+            ml[i] = __ldcg(reinterpret_cast<const float2*>(p));
+            o[i] = __ldcg(reinterpret_cast<const float4*>(p + 4) + lane);
+          }
+          float top = M;
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            if (s0 + i * NEXT >= S) ml[i] = make_float2(-1e30f, 0.0f);
+            top = fmaxf(top, ml[i].x);
+          }
+          const float w0 = ex2(M - top);
+          L *= w0;
+          O.x *= w0;
+          O.y *= w0;
+          O.z *= w0;
+          O.w *= w0;
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            if (s0 + i * NEXT >= S) break;
+            const float w = ex2(ml[i].x - top);
+            L = fmaf(w, ml[i].y, L);
+            O.x = fmaf(w, o[i].x, O.x);
+            O.y = fmaf(w, o[i].y, O.y);
+            O.z = fmaf(w, o[i].z, O.z);
+            O.w = fmaf(w, o[i].w, O.w);
+          }
+          M = top;
         }
       }
-    }
-    if (h < nh && (!ONE || warp == 0)) {
-      const float inv = L != 0.0f ? 1.0f / L : 0.0f;
-      *reinterpret_cast<float4*>(&os[ONE ? 0 : h][4 * lane]) = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-      if (a.lse && lane == 0) a.lse[orow + h] = S ? M * 0.69314718055994531f + logf(L) : -INFINITY;
-    }
-    __syncthreads();
-    float x[32], y[4];
-    lane_share(os[gq], x);
-    rows_times(pt, x, y);
+      if constexpr (ONE) {
+        if (lane == 0) {
+          rm[warp] = M;
+          rl[warp] = L;
+        }
+        *reinterpret_cast<float4*>(&res[warp][4 * lane]) = O;
+        __syncthreads();
+        if (warp == 0) {
+          O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          L = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int col = 2 * t + (i & 1);
-      if (ONE ? col == 0 : col < nh) {
-        const int64_t at = (orow + (ONE ? h0 : col)) * D + 16 * warp + gq + 8 * (i >> 1);
-        if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y[i]);
-        else reinterpret_cast<float*>(a.out)[at] = y[i];
+          for (int k = 0; k < MW; ++k) M = fmaxf(M, rm[k]);
+#pragma unroll
+          for (int k = 0; k < MW; ++k) {
+            const float w = ex2(rm[k] - M);
+            const float4 o = *reinterpret_cast<const float4*>(&res[k][4 * lane]);
+            L = fmaf(w, rl[k], L);
+            O.x = fmaf(w, o.x, O.x);
+            O.y = fmaf(w, o.y, O.y);
+            O.z = fmaf(w, o.z, O.z);
+            O.w = fmaf(w, o.w, O.w);
+          }
+        }
+      }
+      if (!ONE || warp == 0) {
+        const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+        vec.put(ONE ? 0 : HPW * warp + x, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+        if (h.live && a.lse && lane == 0) a.lse[h.row] = S ? M * 0.69314718055994531f + logf(L) : -INFINITY;
       }
     }
-    __syncthreads();  // the next item reuses the vectors
+    __syncthreads();
+    product(pt, vec, res, warp, gq, t);
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < (ONE ? 1 : HPW); ++x) {
+      const int r = ONE ? 0 : HPW * warp + x;
+      const HeadPlace h = head_place(p0 + r, a.hgn, a.hgroups, a.g, a.units);
+      if (!h.live || (ONE && warp)) continue;
+      const float4 v = *reinterpret_cast<const float4*>(&res[r][4 * lane]);
+      if (a.out_bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + h.row * D)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + h.row * D)[lane] = v;
+      }
+    }
+    if constexpr (ONE) __syncthreads();  // (res is the warps' partials again)
   }
 }
 
@@ -434,7 +517,7 @@ int attr_of(cudaDeviceAttr attr, int fallback) {
 struct WsPlan {
   int hgroups, nb;
   int64_t units;
-  size_t ops, part, before, err, bytes;
+  size_t ops, part, before, pit, err, bytes;
 };
 WsPlan ws_plan(int B, int Hq, int Hkv, int ctas) {
   WsPlan w;
@@ -446,7 +529,8 @@ WsPlan ws_plan(int B, int Hq, int Hkv, int ctas) {
   w.ops = 0;
   w.part = up((size_t)w.units * seg_bytes(w.nb));
   w.before = w.part + up((size_t)(w.units + ctas * paged_warps(w.nb)) * 4 * w.nb * PART * 4);
-  w.err = w.before + up((size_t)(B + 1) * 8);
+  w.pit = w.before + up((size_t)(B + 1) * 8);
+  w.err = w.pit + (size_t)MW * 512 * sizeof(uint4);
   w.bytes = w.err + 256;
   return w;
 }
@@ -572,8 +656,10 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   p.lens = seq_lens;
   p.ops = a.ops;
   p.before = a.before;
+  p.pit = reinterpret_cast<uint4*>(ws + w.pit);
   p.err = a.err;
-  st = launch_dep(qjl ? paged_prep<true> : paged_prep<false>, std::min<int64_t>(w.units, sms - 1) + 1, MT, s, false, "paged prep", p);
+  st = launch_dep(qjl ? paged_prep<true> : paged_prep<false>, std::min<int64_t>((w.units * 4 * w.nb + PR - 1) / PR, sms - 1) + 1, MT,
+                  s, false, "paged prep", p);
   if (st != TQ_OK) return st;
   st = pool->k_bits == 2   ? paged_split_k2(a, pool->v_bits, qjl, s)
        : pool->k_bits == 3 ? paged_split_k3(a, pool->v_bits, qjl, s)
@@ -590,13 +676,16 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   m.warps = paged_warps(w.nb);
   m.part = a.part;
   m.before = a.before;
-  m.Pi = params->Pi;
+  m.pit = p.pit;
   m.err = a.err;
   m.out = out;
   m.out_bf16 = out_dtype == TQ_BF16;
   m.lse = lse;
-  // one head per CTA while the units alone would leave SMs idle; two CTAs fit an SM
-  const bool one = w.units < sms;
-  m.items = (int)(one ? w.units * m.hgn : w.units);
-  return launch_dep(one ? paged_merge<true> : paged_merge<false>, std::min<int64_t>(m.items, 2 * sms), MT, s, true, "paged merge", m);
+  m.units = (int)w.units;
+  // Sixteen heads at a time when that gives every CTA (two fit an SM) a round, eight while that fills half
+  // the SMs' CTAs, else one.
+  const int64_t heads = w.units * m.hgn, room = 2 * sms;
+  if (heads >= 16 * room) return launch_dep(paged_merge<2>, room, MT, s, true, "paged merge", m);
+  if (heads >= 4 * room) return launch_dep(paged_merge<1>, std::min<int64_t>(heads / 8, room), MT, s, true, "paged merge", m);
+  return launch_dep(paged_merge<0>, std::min<int64_t>(heads, room), MT, s, true, "paged merge", m);
 }
