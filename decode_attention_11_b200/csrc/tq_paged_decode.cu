@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ Prep
 #pragma unroll
       for (int x = 0; x < 2; ++x) s4[x] = *reinterpret_cast<const float4*>(&ss[2 * warp + x][4 * lane]);
     }
-    // Per head: a power of two 2^-e that brings q' and 16 S q' below 2^14 (fp16 range), and the QJL
+    // Per head: a power of two 2^-e that brings the largest of q' and 16 S q' into [2^13, 2^14), and the QJL
     // constant Kh = -C - 0.5 sum_l sq_l 2^-e, C the sum of the fp16 parts of the pre-scaled S q':
     // sum_l sq_l (2 b_l - 1) = 2 (D_hi + D_lo + Kh) in the split kernel's product.
     // Then the head's fragments: k-step kk holds k = 16kk + 2t, + 1 (register 0), + 8, + 9 (register 1)
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ Prep
       for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(qv[i]), 16.0f * fabsf(sv[i])));
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-      const int ex = (mx < 16384.0f || !(mx < INFINITY)) ? 0 : ((__float_as_int(mx) >> 23) & 255) - 127 - 13;
+      const int ex = !(mx < INFINITY) ? 0 : max(((__float_as_int(mx) >> 23) & 255) - 127, -90) - 13;
       const float dn = __int_as_float((127 - ex) << 23);
       const float scl = (float)(16 >> ((lane >> 1) & 3));  // sgn_scale of the lane's k-step pair
       uint32_t qh[2], ql[2], sh[2], sl[2];

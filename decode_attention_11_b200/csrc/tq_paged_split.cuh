@@ -23,9 +23,10 @@
 // with online softmax in log2 units in between.  q' and the weights enter as fp16 hi + lo (about 22
 // bits), sums are fp32.  The 8 columns of B are four heads, hi and lo side by side (one product), or,
 // for five to eight heads, eight heads, hi and lo in two products onto the same sums: that keeps the
-// sums at 32 registers.  The running maximum moves only when a score passes it by more than
-// LAZY (a vote instead of a three-step exchange per group): weights reach 2^LAZY, which the value scale
-// takes back so that they stay as far inside fp16 range as weights of at most 1.
+// sums at 32 registers.  The running maximum moves only when a score passes it by more than LAZY (a vote
+// instead of a three-step exchange per group), so exp reaches 2^LAZY.  The weights carry a power of two
+// that brings them into fp16 range whatever the values' norms are; it moves, by the same vote, when a
+// norm outgrows it.
 // Rows outside the tokens shown are masked by selection, never by a product, so whatever they hold
 // (NaN too) stays out.
 #pragma once
@@ -39,7 +40,10 @@ namespace tq {
 namespace {
 
 constexpr float LAZY = 4.0f;
-constexpr float LAZY_SCALE = 1.0f / 16.0f;  // 2^-LAZY
+// exponent of the largest value norm times its scale when that is set, and the bound at which it is set
+// anew: times 2^LAZY that stays below fp16's 65504
+constexpr int NORM_EXP = 8;
+constexpr float NORM_LIMIT = 2048.0f;
 constexpr int P_LENS = 512;                 // sequences whose lengths and running sums are kept in shared memory
 constexpr int P_SMEM = 232448;              // dynamic shared memory of a CTA (all an SM gives one)
 constexpr int P_MISC = 8192;                // lengths, sums, codebooks
@@ -393,6 +397,7 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
   // ([2], [3]).
   float oacc[8][4];
   float m_run[H], l_run[H];
+  float vscale = 1.0f, vlimit = -1.0f;  // weights are exp * norm * vscale; the largest norm that fits
   while (left > 0) {
     const int64_t unit = (int64_t)cur.b * U + cur.uu;
     const bool opens = cur.gi == 0;
@@ -433,6 +438,8 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
       m_run[x] = -1e30f;  // finite: ex2(s - m) and ex2(m_old - m_new) never see inf - inf
       l_run[x] = 0.0f;
     }
+    vscale = 1.0f;
+    vlimit = -1.0f;  // (the first group sets them)
     int tk = kGroup * (cur.first / kGroup + cur.gi) + gq - cur.first;  // row gq's place among the tokens shown
     const uint32_t shown = (uint32_t)(cur.len - cur.first);
     for (; n > 0; --n, tk += kGroup) {
@@ -488,11 +495,9 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
         rn0 = ldf<Lay::OFF_RN - Lay::OFF_NK>(np);
         rn1 = ldf<Lay::OFF_RN - Lay::OFF_NK + 32>(np);
       }
-      constexpr float VSC = 0.08838834764831845f * LAZY_SCALE;  // 1 / sqrt(128)
-      const float nv0 = v0ok ? ldf<64>(np) * VSC : 0.0f;
-      const float nv1 = v1ok ? ldf<96>(np) * VSC : 0.0f;
+      const float nv0 = v0ok ? ldf<64>(np) : 0.0f, nv1 = v1ok ? ldf<96>(np) : 0.0f;
       float sc0[H], sc1[H];  // scores of the two tokens
-      bool over = false;
+      bool over = fmaxf(nv0, nv1) > vlimit;
 #pragma unroll
       for (int x = 0; x < H; ++x) {
         // a head's sum: its columns hi + lo, or its column of the blocks hi + lo
@@ -509,7 +514,22 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
         sc1[x] = v1ok ? s1v : -INFINITY;
         over = over || fmaxf(sc0[x], sc1[x]) > m_run[x] + LAZY;
       }
-      if (__any_sync(FULL, over)) {  // the running maximum of some head moves
+      if (__any_sync(FULL, over)) {  // the running maximum of some head moves, or the norms' scale
+        float nm = fmaxf(nv0, nv1);
+        nm = fmaxf(nm, __shfl_xor_sync(FULL, nm, 4));
+        nm = fmaxf(nm, __shfl_xor_sync(FULL, nm, 8));
+        nm = fmaxf(nm, __shfl_xor_sync(FULL, nm, 16));
+        if (nm > vlimit) {  // warp-uniform
+          const int e = max(((__float_as_int(nm) >> 23) & 255) - 127, -100);
+          const float now = __int_as_float((127 + NORM_EXP - e) << 23);
+          const float r = vlimit < 0.0f ? 0.0f : now / vscale;  // (nothing has been summed yet)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) oacc[i][j] *= r;
+          vscale = now;
+          vlimit = NORM_LIMIT / now;
+        }
 #pragma unroll
         for (int x = 0; x < H; ++x) {
           float mx = fmaxf(sc0[x], sc1[x]);
@@ -541,8 +561,8 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
           const float e0 = ex2(sc0[x] - m_run[x]);  // ex2(-inf) = 0 for rows that are not shown
           const float e1 = ex2(sc1[x] - m_run[x]);
           l_run[x] += e0 + e1;
-          p0[x] = e0 * nv0;
-          p1[x] = e1 * nv1;
+          p0[x] = e0 * (nv0 * vscale);
+          p1[x] = e1 * (nv1 * vscale);
         }
         if constexpr (NB == 1) {
           bp[0][0] = movmatrix_trans(hilo_half2(p0[0]));
@@ -616,6 +636,11 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
       l_run[x] += __shfl_xor_sync(FULL, l_run[x], 8);
       l_run[x] += __shfl_xor_sync(FULL, l_run[x], 16);
     }
+    const float vback = 0.08838834764831845f / vscale;  // with the values' 1 / sqrt(128)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) oacc[i][j] *= vback;
     if (joint) break;  // (the range's only segment)
 #pragma unroll
     for (int x = 0; x < H; ++x) {
@@ -625,8 +650,8 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
       for (int db = 0; db < 8; ++db) {
         const float o0 = NB == 1 ? oacc[db][0] + oacc[db][1] : oacc[db][x];
         const float o1 = NB == 1 ? oacc[db][2] + oacc[db][3] : oacc[db][2 + x];
-        dst[4 + 16 * db + gq] = o0 * (1.0f / LAZY_SCALE);
-        dst[4 + 16 * db + 8 + gq] = o1 * (1.0f / LAZY_SCALE);
+        dst[4 + 16 * db + gq] = o0;
+        dst[4 + 16 * db + 8 + gq] = o1;
       }
     }
   }
@@ -668,7 +693,7 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
         O = fmaf(fw, v[2 * HGN + i * D + dd], O);
       }
       float* dst = a.part + (rec_joint * HGN + i) * PART;
-      dst[4 + dd] = O * (1.0f / LAZY_SCALE);
+      dst[4 + dd] = O;
       if (dd == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, Ls);
     }
   }

@@ -158,6 +158,63 @@ def test_decode_long_and_many(B, Hkv, Hq, lens):
     assert_close(out, lse, *reference(q, pool, table, lens))
 
 
+@pytest.mark.parametrize("kb", [2, 3, 4])
+@pytest.mark.parametrize("vb", [2, 3, 4])
+@pytest.mark.parametrize("qjl", [True, False])
+@pytest.mark.parametrize("Hq", [2, 6])
+def test_decode_every_width(kb, vb, qjl, Hq):
+    """Every pair of widths, with and without a sketch, up to four and up to eight heads per kv-head."""
+    ps, lens = 16, [33, 5]
+    pool = filled_pool(5, 1, ps, kb, vb, qjl, seed=kb + vb)
+    table = table_for(lens, ps, 5)
+    q = queries(2, Hq)
+    out, lse = tq.paged_decode_attn(params(kb, vb, qjl), q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    assert_close(out, lse, *reference(q, pool, table, lens, qjl=qjl))
+
+
+@pytest.mark.parametrize("vs,ks", [(1e-20, 1.0), (1e-6, 1e-5), (1e7, 1e6), (1e25, 1e15), ("growing", 1.0), ("falling", 1e-3)])
+def test_decode_scales(vs, ks):
+    """Values and keys of any magnitude (queries the other way, so that scores stay as they are); value norms
+    that grow, or fall, by 2^40 along a sequence; zero values first."""
+    ps, lens = 32, [700, 40]
+    pages = 24
+    pool = filled_pool(pages, 1, ps, 4, 4)
+    table = table_for(lens, ps, pages)
+    if isinstance(vs, str):
+        for b, n in enumerate(lens):
+            t = torch.arange(n, device="cuda")
+            x = 2.0 ** (40.0 * (t if vs == "growing" else n - t) / n - 20)
+            x[:17] = 0
+            pool.v_norm[table[b, t // ps].long(), 0, t % ps] = x.float()
+    else:
+        pool.v_norm *= vs
+    pool.k_norm *= ks
+    pool.k_rnorm *= ks
+    q = queries(2, 6) / ks
+    out, lse = tq.paged_decode_attn(params(4, 4), q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    assert_close(out, lse, *reference(q, pool, table, lens))
+
+
+def test_decode_batch_past_shared_memory():
+    """More sequences than a CTA keeps the lengths of; empty ones in between and at both ends."""
+    B, ps = 700, 16
+    r = np.random.RandomState(3)
+    lens = r.randint(0, 60, B)
+    lens[r.rand(B) < 0.3] = 0
+    lens[0] = lens[-1] = lens[300:340] = 0
+    lens = lens.tolist()
+    pages = sum(-(-n // ps) for n in lens) + 1
+    pool = filled_pool(pages, 1, ps, 3, 3)
+    table = table_for(lens, ps, pages)
+    q = queries(B, 2)
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for w in (0, 20):
+        out, lse = tq.paged_decode_attn(params(3, 3), q, pool, table, lt, window=w, return_lse=True)
+        assert_close(out, lse, *reference(q, pool, table, lens, w))
+
+
 def test_decode_ignores_what_is_not_shown():
     """NaN norms and any codes in rows past the length, before the window, and in pages of no sequence."""
     ps, lens, window = 32, [45, 100, 0, 64], 40
@@ -359,6 +416,38 @@ def test_quantize_rows(kb, vb, qjl, dtype, N, Hkv, ps):
             a = getattr(pool, n)
             a = a.view(torch.uint8).view(pages, Hkv, ps, -1)
             assert (a[rest] == 0xA5).all(), n
+
+
+@pytest.mark.parametrize("N", [24, 1700])
+def test_quantize_in_a_graph_and_on_a_stream(N):
+    """Both routes captured: a replay quantizes the inputs and slots as they are then; nothing to do for N = 0."""
+    K, V = (torch.randn(N, 3, 128, device="cuda").to(torch.bfloat16) for _ in range(2))
+    p, pool = params(4, 4), tq.Cache.allocate(-(-N // 16) + 2, 3, 16, 4, 4)
+    slots = torch.arange(N, device="cuda", dtype=torch.int32)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        tq.paged_quantize(p, K, V, pool, slots)
+    for _ in range(2):
+        K.copy_(torch.randn(N, 3, 128, device="cuda"))
+        slots.copy_(torch.randperm(pool.B * 16, device="cuda")[:N])
+        g.replay()
+        check_rows(pool, slots, K, V, 4, 4, True)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    other = tq.Cache.allocate(pool.B, 3, 16, 4, 4)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        tq.paged_quantize(p, K, V, pool, slots, stream=a)
+        tq.paged_quantize(p, V, K, other, slots, stream=b)
+    torch.cuda.synchronize()
+    check_rows(pool, slots, K, V, 4, 4, True)
+    check_rows(other, slots, V, K, 4, 4, True)
+    before = [getattr(pool, n).clone() for n in ARRAYS]
+    tq.paged_quantize(p, K[:0], V[:0], pool, slots[:0])
+    k, v, sg, rn = tq.paged_read(p, pool, slots[:0])
+    assert k.shape == v.shape == sg.shape == (0, 3, 128) and rn.shape == (0, 3)
+    assert all(torch.equal(a, getattr(pool, n)) for a, n in zip(before, ARRAYS))
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
