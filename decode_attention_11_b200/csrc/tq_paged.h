@@ -12,14 +12,14 @@ namespace tq {
 
 constexpr int kGroup = kPageTokens;  // tokens of a group: the unit of work, inside one page
 
-// Warps of a split CTA: 12, three per scheduler with 168 registers a thread.  (Four heads per unit at 128K x 4:
-// 168 us, against 185 us with 8 or 16 warps and 190 to 215 us with 13 to 15, which load schedulers unevenly;
-// eight heads: 139 us with 8 or 12, 146 to 177 us with 4, 9, 10 or 11.)
+// Warps of a split CTA: multiples of four, so that its schedulers are loaded alike.  Up to four heads per
+// unit (nb = 1): 12 warps of 168 registers (128K x 4 in 4 bits: 168 us; 8 or 16 warps 185 us, 13 to 15 190 to
+// 215 us).  Up to eight: 8 warps of 255 (64 sequences to 16K, 3/2 bits: 121 us; 12 warps 127 us, 4 warps 177 us).
 #ifndef PNW1
 #define PNW1 12
 #endif
 #ifndef PNW2
-#define PNW2 12
+#define PNW2 8
 #endif
 constexpr int paged_warps(int nb) { return nb == 1 ? PNW1 : PNW2; }
 

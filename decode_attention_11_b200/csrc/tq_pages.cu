@@ -26,7 +26,8 @@ constexpr int MAX_CACHES = 64;                 // pools of one launch (their poi
 constexpr unsigned FULL = 0xffffffffu;
 
 // ------------------------------------------------------------------------------------- workspace
-// int32 words: [0] pages to copy, [1] the plan's go-ahead, then the arrays below.
+// int32 words: [0] pages to copy (compact: pages in use), [1] the plan's go-ahead, [2] compact: pages in
+// use that stay; then the arrays below.
 struct Ws {
   int32_t* head;
   int32_t* need;   // [n + 1] pages before entry i
@@ -36,7 +37,7 @@ struct Ws {
   int32_t* room;   // [num_pages] free pages in order
   int32_t* from;   // [max(n, num_pages)] copy pairs
   int32_t* to;
-  int32_t* map;    // [num_pages] the page, or -1 - its place in from[]
+  int32_t* map;    // [num_pages] the page, or -1 - its place in from[] (compact)
 };
 __host__ __device__ inline size_t ws_words(int n, int n_seq, int pages) {
   const size_t pairs = n > pages ? n : pages;
@@ -87,43 +88,62 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t& total) {
   return part[warp] + x - v;
 }
 
-// The plan's threads take contiguous shares of the pages, whole 16-byte words: share [begin, end) of
-// thread tid.  (A share per thread needs one scan over the CTA, where chunks of 4096 pages in turn took
-// one each: 18 us for 16K pages.)
-__device__ __forceinline__ void share_of(int pages, int& begin, int& end) {
-  const int per = (pages + 4 * PLAN_THREADS - 1) / (4 * PLAN_THREADS) * 4;
-  begin = (int)min((int64_t)threadIdx.x * per, (int64_t)pages);
-  end = min(begin + per, pages);
-}
-// f(p, refs[p]) for the pages of a share, four to a load.
-template <typename F>
-__device__ __forceinline__ void each_page(const int32_t* refs, int begin, int end, F&& f) {
-  int p = begin;
-#pragma unroll 2
-  for (; p + 4 <= end; p += 4) {
-    const int4 r = *reinterpret_cast<const int4*>(refs + p);
-    f(p, r.x);
-    f(p + 1, r.y);
-    f(p + 2, r.z);
-    f(p + 3, r.w);
+// A plan's warps take contiguous shares of the pages, a lane a page, so that a ballot ranks 32 of them and
+// one scan over the warps' counts the rest.  (Chunks of 4096 pages in turn, a scan each, took 18 us for 16K
+// pages; contiguous pages per thread, whose loads and stores do not coalesce, 22 us.)
+constexpr int PLAN_WARPS = PLAN_THREADS / 32;
+struct PageShare {
+  int begin, rounds;  // first page and rounds of 32 pages
+  __device__ __forceinline__ explicit PageShare(int pages) {
+    rounds = (pages + 32 * PLAN_WARPS - 1) / (32 * PLAN_WARPS);
+    begin = (int)(threadIdx.x >> 5) * rounds * 32;
   }
-  for (; p < end; ++p) f(p, refs[p]);
+  // f(p, used, ballot of used) for every round, the whole warp together (used is false past the last page)
+  template <typename F>
+  __device__ __forceinline__ void each(const int32_t* refs, int pages, F&& f) const {
+    const int lane = threadIdx.x & 31;
+    for (int r0 = 0; r0 < rounds; r0 += 8) {
+      int v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // eight rounds' loads together
+        const int64_t p = (int64_t)begin + 32 * (r0 + j) + lane;
+        v[j] = r0 + j < rounds && p < pages ? refs[p] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (r0 + j < rounds) {
+          const unsigned m = __ballot_sync(FULL, v[j] > 0);
+          f((int64_t)begin + 32 * (r0 + j) + lane, v[j] > 0, m);
+        }
+    }
+  }
+};
+__device__ __forceinline__ int below_lane(unsigned m) { return __popc(m & ((1u << (threadIdx.x & 31)) - 1u)); }
+// Exclusive prefix sum over the warps of a count that is the same in all lanes, and its total.
+__device__ __forceinline__ int64_t warp_counts(int n, int64_t& total) {
+  const int lane = threadIdx.x & 31;
+  const int64_t at = block_scan(lane == 0 ? n : 0, total);
+  return __shfl_sync(FULL, at, 0);
 }
 
 // The first `need` free pages in order to room[]; returns how many free pages there are.
 __device__ int64_t free_pages(const tq_page_table& pt, int64_t need, int32_t* room) {
-  int begin, end;
-  share_of(pt.num_pages, begin, end);
+  const PageShare share(pt.num_pages);
+  auto is_free = [&](int64_t p, unsigned used) {  // free pages of the round, without those past the last page
+    const int64_t first = p - (threadIdx.x & 31);
+    const unsigned real = first + 32 <= pt.num_pages ? FULL : first >= pt.num_pages ? 0u : (1u << (pt.num_pages - first)) - 1u;
+    return ~used & real;
+  };
   int mine = 0;
-  each_page(pt.refs, begin, end, [&](int, int r) { mine += r <= 0; });
+  share.each(pt.refs, pt.num_pages, [&](int64_t p, bool, unsigned m) { mine += __popc(is_free(p, m)); });
   int64_t total;
-  int64_t at = block_scan(mine, total);
+  int64_t at = warp_counts(mine, total);
   if (mine && at < need)
-    each_page(pt.refs, begin, end, [&](int p, int r) {
-      if (r <= 0) {
-        if (at < need) room[at] = p;
-        ++at;
-      }
+    share.each(pt.refs, pt.num_pages, [&](int64_t p, bool, unsigned m) {
+      const unsigned f = is_free(p, m);
+      const int64_t r = at + below_lane(f);
+      if (((f >> (threadIdx.x & 31)) & 1u) && r < need) room[r] = (int32_t)p;
+      at += __popc(f);
     });
   return total;
 }
@@ -410,50 +430,44 @@ __global__ void __launch_bounds__(COPY_THREADS) free_seqs(const tq_page_table pt
 __global__ void __launch_bounds__(PLAN_THREADS) compact_plan(const tq_page_table pt, int32_t* wsp) {
   const Ws w = ws_at(wsp, 0, pt.n_seq, pt.num_pages);
   const int tid = threadIdx.x, P = pt.num_pages;
-  __shared__ int below;  // pages in use with a number below `live`
   pdl_launch();
-  int begin, end, mine = 0;
-  share_of(P, begin, end);
-  each_page(pt.refs, begin, end, [&](int, int r) { mine += r > 0; });
+  const PageShare share(P);
+  int mine = 0;
+  share.each(pt.refs, P, [&](int64_t, bool, unsigned m) { mine += __popc(m); });
   int64_t live;
-  const int before = (int)block_scan(mine, live);  // pages in use before the share
-  if (live == P && tid == 0) below = (int)live;
-  if (begin <= live && live < end) {
-    int n = before;
-    each_page(pt.refs, begin, (int)live, [&](int, int r) { n += r > 0; });
-    below = n;
-  }
-  __syncthreads();
-  // free numbers below `live` (to) and pages in use from `live` on (from), each in order: as many of
-  // the ones as of the others
-  const int movers = (int)live - below;
-  int n = before;
-  auto one = [&](int p, int r) {  // (map: the page itself, or -1 - its place among the movers)
-    int m = p;
-    if (r > 0) {
-      if (p >= live) {
-        w.from[n - below] = p;
-        m = -1 - (n - below);
+  int n = (int)warp_counts(mine, live);  // pages in use before the share, then before the round
+  // Free numbers below `live` to to[], in order; pages in use to from[], at their rank among all in use:
+  // the j-th mover is from[below + j], below (head[2]) the number of pages in use below `live`.
+  share.each(pt.refs, P, [&](int64_t p, bool used, unsigned m) {
+    const int rank = n + below_lane(m);  // pages in use before p
+    if (p < P) {
+      int to = (int)p;
+      if (used && p >= live) {
+        w.from[rank] = (int32_t)p;
+        to = -1 - rank;
+      } else if (!used && p < live) {
+        w.to[p - rank] = (int32_t)p;
       }
-      ++n;
-    } else if (p < live) {
-      w.to[p - n] = p;
+      w.map[p] = to;
+      if (p == live) w.head[2] = rank;
     }
-    return m;
-  };
-  each_page(pt.refs, begin, end, [&](int p, int r) { w.map[p] = one(p, r); });
-  if (tid == 0) w.head[0] = movers;
+    n += __popc(m);
+  });
+  if (tid == 0) {
+    w.head[0] = (int32_t)live;
+    if (live == P) w.head[2] = P;
+  }
 }
 
 __global__ void __launch_bounds__(COPY_THREADS)
     compact_apply(const tq_page_table pt, bool rows, const __grid_constant__ CopyArgs a, int32_t* wsp) {
   const Ws w = ws_at(wsp, 0, pt.n_seq, pt.num_pages);
   pdl_wait();
-  const int moved = w.head[0];
+  const int below = w.head[2], moved = w.head[0] - below;
   if (moved == 0) return;
   for (int i = blockIdx.x * COPY_THREADS + threadIdx.x; rows && i < moved; i += gridDim.x * COPY_THREADS) {
-    pt.refs[w.to[i]] = pt.refs[w.from[i]];
-    pt.refs[w.from[i]] = 0;
+    pt.refs[w.to[i]] = pt.refs[w.from[below + i]];
+    pt.refs[w.from[below + i]] = 0;
   }
   const int64_t entries = (int64_t)pt.n_seq * pt.max_pages;
   for (int64_t i = (int64_t)blockIdx.x * COPY_THREADS + threadIdx.x; rows && i < entries;
@@ -461,9 +475,9 @@ __global__ void __launch_bounds__(COPY_THREADS)
     const int p = pt.table[i];
     if ((unsigned)p >= (unsigned)pt.num_pages) continue;
     const int q = w.map[p];
-    if (q < 0) pt.table[i] = w.to[-1 - q];
+    if (q < 0) pt.table[i] = w.to[-1 - q - below];
   }
-  copy_pairs(a, w.from, w.to, moved, 0, nullptr);
+  copy_pairs(a, w.from + below, w.to, moved, 0, nullptr);
 }
 
 // ------------------------------------------------------------------------------------- host
