@@ -15,13 +15,7 @@ constexpr int kGroup = kPageTokens;  // tokens of a group: the unit of work, ins
 // Warps of a split CTA: multiples of four, so that its schedulers are loaded alike.  Up to four heads per
 // unit (nb = 1): 12 warps of 168 registers (128K x 4 in 4 bits: 168 us; 8 or 16 warps 185 us, 13 to 15 190 to
 // 215 us).  Up to eight: 8 warps of 255 (64 sequences to 16K, 3/2 bits: 121 us; 12 warps 127 us, 4 warps 177 us).
-#ifndef PNW1
-#define PNW1 12
-#endif
-#ifndef PNW2
-#define PNW2 8
-#endif
-constexpr int paged_warps(int nb) { return nb == 1 ? PNW1 : PNW2; }
+constexpr int paged_warps(int nb) { return nb == 1 ? 12 : 8; }
 
 // Groups of 16 tokens that hold the tokens [first, len) a sequence of length n shows; a length outside
 // [0, max_tokens] counts as 0.
@@ -50,7 +44,9 @@ __host__ __device__ inline Cut cut_of(int64_t N, int ctas, int most_warps) {
   c.ctas = n < 1 ? 1 : n > ctas ? ctas : (int)n;
   return c;
 }
-__host__ __device__ inline int64_t range_start(int64_t N, const Cut& c, int64_t W) { return div64(W * N, (int64_t)c.ctas * c.warps); }
+__host__ __device__ inline int64_t range_start(int64_t N, const Cut& c, int64_t W) {
+  return div64(W * N, (int64_t)c.ctas * c.warps);
+}
 // the warp whose range holds group f
 __host__ __device__ inline int range_of(int64_t N, const Cut& c, int64_t f) {
   return (int)div64((f + 1) * ((int64_t)c.ctas * c.warps) - 1, N);
@@ -62,7 +58,7 @@ __host__ __device__ inline int range_of(int64_t N, const Cut& c, int64_t f) {
 __host__ __device__ constexpr int seg_bytes(int nb) { return nb * (4096 + 4 * 16); }
 
 struct PagedArgs {
-  int B, Hq, Hkv, g, hgroups;
+  int B, Hkv, g, hgroups;
   int pages, ps;          // of the pool
   uint64_t gpp_inv;       // ceil(2^64 / groups per page): group / groups per page by one product
   int64_t table_stride;

@@ -181,7 +181,7 @@ __device__ __forceinline__ HeadPlace head_place(int p, int hgn, int hgroups, int
 constexpr int PR = 16;  // heads of a CTA at a time, two per warp
 
 struct PrepArgs {
-  int B, Hq, Hkv, g, hgroups, nb;
+  int B, g, hgroups, nb;
   int units, max_tokens, window;
   float sK, sQ;
   const void* q;
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ Prep
 // heads to fill the SMs: one head, whose partials the eight warps share.
 
 struct MergeArgs {
-  int B, Hq, Hkv, g, hgroups, hgn, ctas, warps, units;
+  int B, Hkv, g, hgroups, hgn, ctas, warps, units;
   const float* part;
   const int64_t* before;
   const uint4* pit;
@@ -613,7 +613,6 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
 
   PagedArgs a;
   a.B = B;
-  a.Hq = Hq;
   a.Hkv = pool->Hkv;
   a.g = Hq / pool->Hkv;
   a.hgroups = w.hgroups;
@@ -643,8 +642,6 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
 
   PrepArgs p;
   p.B = B;
-  p.Hq = Hq;
-  p.Hkv = pool->Hkv;
   p.g = a.g;
   p.hgroups = w.hgroups;
   p.nb = w.nb;
@@ -672,7 +669,6 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   if (st != TQ_OK) return st;
   MergeArgs m;
   m.B = B;
-  m.Hq = Hq;
   m.Hkv = pool->Hkv;
   m.g = a.g;
   m.hgroups = w.hgroups;

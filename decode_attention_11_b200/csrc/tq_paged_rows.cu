@@ -48,9 +48,11 @@ struct RowArgs {
 };
 
 constexpr int ROWS = 4;
-// Rows per SM up to which the fp64 kernel is used (about 0.5 us a row and SM, against the pipeline's
-// fixed cost).
-constexpr int kRowKernelPerSm = 32;
+// Rows per SM up to which the fp64 kernel is used.  It takes 16 us for up to four rows per SM and 10 us for
+// each four more (caches cold, by itself), whatever the rows hold.  The bf16 pipeline takes 32 to 38 us at
+// eight (by widths; up to 47 with rows that its fixups have to do anew), 30 to 38 at twelve against 36; the
+// general kernel that fp32 rows go to takes 46 to 74 us at sixteen against 45, 46 to 76 at twenty against 55.
+constexpr int kRowsPerSmBf16 = 8, kRowsPerSmF32 = 16;
 constexpr int QT = 256;    // eight warps of 16 matrix rows
 constexpr int XS = D + 2;  // stride of a vector in shared memory (in doubles; no bank conflicts)
 
@@ -252,7 +254,7 @@ constexpr int RT = 256;
 
 template <int KB, int VB, typename T>
 __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs a) {
-  const uint32_t r = (blockIdx.x * (uint32_t)RT + threadIdx.x) >> 3;  // (at most 2^30 rows)
+  const uint32_t r = blockIdx.x * (uint32_t)(RT / 8) + (threadIdx.x >> 3);  // (at most 2^30 rows)
   const int p = threadIdx.x & 7;
   const bool live = r < (uint32_t)a.N * (uint32_t)a.Hkv;
   int64_t row = -1;
@@ -371,7 +373,7 @@ extern "C" tq_status tq_paged_quantize(const tq_params* params, const void* k, c
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "device query: %s", cudaGetErrorString(e));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = (int64_t)N * pool->Hkv;
-  if (rows > (int64_t)kRowKernelPerSm * sms) {
+  if (rows > (int64_t)(dtype == TQ_BF16 ? kRowsPerSmBf16 : kRowsPerSmF32) * sms) {
     if (dtype == TQ_BF16) {
       bool handled = false;
       st = quantize_bf16_pipeline(params, k, v, 0, stride_h, stride_n, N, 0, slots, pool, sms, s, &handled);

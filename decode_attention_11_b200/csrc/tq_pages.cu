@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(COPY_THREADS)
     pt.refs[p] = 1;
   }
   for (int i = first; ok && i < n; i += step) pt.seq_lens[seqs[i]] = w.old[i] + grow[i];
-  for (int t = first; t < n_slots; t += step) {
+  for (int64_t k = first; k < n_slots; k += step) {
+    const int t = (int)k;
     int v = -1;
     if (t < toks) {
       const int i = entry_of(w.tok, n, t), pos = w.old[i] + t - w.tok[i], page = pos / ps;

@@ -426,7 +426,9 @@ tq_status tq_pages_reserve(const tq_page_table* pt, const int32_t* seqs, const i
  * filled last page is copied, in every pool of `caches`, to a page of its own, so that both can grow.
  *   src, dst  device int32 [n]; the dst distinct, empty, and in no src place
  *   caches    n_caches pools (all layers of the model) of equal sizes, B = num_pages, T_cap = page_size
- * On an error (NO_ROOM, BAD_INDEX, NOT_EMPTY, BAD_LENGTH) nothing changes.
+ * On an error (NO_ROOM, BAD_INDEX, NOT_EMPTY, BAD_LENGTH) nothing changes.  (A page number out of range
+ * among the full pages of a source, in a table that was written by other means, is recorded as
+ * BAD_INDEX and copied as it is.)
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA.
  */
 tq_status tq_pages_fork(const tq_page_table* pt, const int32_t* src, const int32_t* dst, int n,

@@ -158,6 +158,24 @@ def test_decode_long_and_many(B, Hkv, Hq, lens):
     assert_close(out, lse, *reference(q, pool, table, lens))
 
 
+@pytest.mark.parametrize("B,Hkv,Hq,window", [(600, 2, 8, 0), (520, 2, 10, 9)])
+def test_decode_large_batches(B, Hkv, Hq, window):
+    """More sequences than a CTA keeps lengths of (512), and enough heads for the merge kernel's widest form;
+    one sequence in three is empty."""
+    ps = 16
+    r = np.random.RandomState(B)
+    lens = (r.randint(1, 70, B) * (r.randint(0, 3, B) > 0)).tolist()
+    lens[0] = lens[-1] = 0
+    pages = sum(-(-n // ps) for n in lens) + 1
+    pool = filled_pool(pages, Hkv, ps, 3, 2, seed=B)
+    table = table_for(lens, ps, pages)
+    q = queries(B, Hq)
+    out, lse = tq.paged_decode_attn(params(3, 2), q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    window=window, return_lse=True)
+    assert_close(out, lse, *reference(q, pool, table, lens, window))
+    assert tq.decode_device_errors() == 0
+
+
 @pytest.mark.parametrize("kb", [2, 3, 4])
 @pytest.mark.parametrize("vb", [2, 3, 4])
 @pytest.mark.parametrize("qjl", [True, False])
