@@ -23,7 +23,7 @@
 // with online softmax in log2 units in between.  q' and the weights enter as fp16 hi + lo (about 22
 // bits), sums are fp32.  The sums over tokens are formed on the FP32 units, 16 tokens at a time: the
 // tensor cores cut off instead of rounding, always towards zero, which over 128K tokens left an error of
-// 6.3e-6 where this leaves 1.8e-6 (four sequences of that length: 168 us, 165 with the tensor cores' sums).
+// 6.3e-6 where this leaves 1.8e-6 (four sequences of that length: 171 us, 165 with the tensor cores' sums).
 // The 8 columns of B are four heads, hi and lo side by side (one product), or, for five to eight heads,
 // eight heads, hi and lo in two products onto the same sums: that keeps the sums at 32 registers.  The
 // running maximum moves only when a score passes it by more than LAZY (a vote instead of a three-step
