@@ -254,6 +254,8 @@ constexpr int RT = 256;
 
 template <int KB, int VB, typename T>
 __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs a) {
+  constexpr int PITCH = 16 * (KB + VB) + 16;  // packed codes of a row (the fields of four rows in different banks)
+  __shared__ __align__(16) unsigned char rows[RT / 8][PITCH];
   const uint32_t r = blockIdx.x * (uint32_t)(RT / 8) + (threadIdx.x >> 3);  // (at most 2^30 rows)
   const int p = threadIdx.x & 7;
   const bool live = r < (uint32_t)a.N * (uint32_t)a.Hkv;
@@ -264,36 +266,37 @@ __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs
   }
   // the codebooks, an entry per lane: a lookup is a shuffle (so whole warps stay to the end)
   const float kc = __ldg(a.kc + (threadIdx.x & ((1 << KB) - 1))), vc = __ldg(a.vc + (threadIdx.x & ((1 << VB) - 1)));
-  uint32_t kq[4] = {0, 0, 0, 0}, vq[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  unsigned char* mine = rows[threadIdx.x >> 3];
   uint4 sg = make_uint4(0, 0, 0, 0);
   float kn = 0.0f, vn = 0.0f, rn = 0.0f;
   if (row >= 0) {
-    // key codes: 4 KB bits at bit KB (32t + 4p); value codes: 2 VB bits at bit VB (16g + 2p)
-    const uint8_t* kr = a.k_codes + row * (16 * KB) + (4 * KB * p) / 8;
-    const uint8_t* vr = a.v_codes + row * (16 * VB) + (2 * VB * p) / 8;
-    const int ks = (4 * KB * p) & 7, vs = (2 * VB * p) & 7;
-    const bool v2 = VB == 3 && vs + 6 > 8;  // the field goes on in the next byte
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if constexpr (KB == 4) kq[t] = *reinterpret_cast<const uint16_t*>(kr + 16 * t);
-      else if constexpr (KB == 2) kq[t] = kr[8 * t];
-      else kq[t] = (uint32_t)kr[12 * t] | (uint32_t)kr[12 * t + 1] << 8;
-    }
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      vq[g] = vr[2 * VB * g];
-      if (VB == 3 && v2) vq[g] |= (uint32_t)vr[2 * VB * g + 1] << 8;
+    if (p < KB + VB) {
+      const uint8_t* src = p < KB ? a.k_codes + row * (16 * KB) + 16 * p : a.v_codes + row * (16 * VB) + 16 * (p - KB);
+      *reinterpret_cast<uint4*>(mine + 16 * p) = __ldg(reinterpret_cast<const uint4*>(src));
     }
     if (a.signs) sg = *reinterpret_cast<const uint4*>(a.k_signs + row * 16);
     kn = a.k_norm[row] * 0.08838834764831845f;  // 1 / sqrt(128)
     vn = a.v_norm[row] * 0.08838834764831845f;
     if (a.rnorm) rn = a.k_rnorm[row];
-    if constexpr (KB == 3)
+  }
+  __syncwarp();
+  uint32_t kq[4] = {0, 0, 0, 0}, vq[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (row >= 0) {
+    // key codes: 4 KB bits at bit KB (32t + 4p); value codes: 2 VB bits at bit VB (16g + 2p)
+    const unsigned char* kr = mine + (4 * KB * p) / 8;
+    const unsigned char* vr = mine + 16 * KB + (2 * VB * p) / 8;
+    const int ks = (4 * KB * p) & 7, vs = (2 * VB * p) & 7;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) kq[t] >>= ks;
-    if constexpr (VB != 4)
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (KB == 4) kq[t] = *reinterpret_cast<const uint16_t*>(kr + 16 * t);
+      else if constexpr (KB == 2) kq[t] = kr[8 * t];
+      else kq[t] = ((uint32_t)kr[12 * t] | (uint32_t)kr[12 * t + 1] << 8) >> ks;
+    }
 #pragma unroll
-      for (int g = 0; g < 8; ++g) vq[g] >>= vs;
+    for (int g = 0; g < 8; ++g) {
+      if constexpr (VB == 3) vq[g] = ((uint32_t)vr[6 * g] | (uint32_t)vr[6 * g + 1] << 8) >> vs;  // (the byte behind the row: the pad)
+      else vq[g] = vr[2 * VB * g] >> vs;
+    }
   }
   float v[16];
 #pragma unroll
