@@ -204,7 +204,10 @@ __global__ void __launch_bounds__(QT, 1) quantize_rows(const __grid_constant__ R
 // Eight lanes per row, lane part p holding coordinates 16p .. 16p + 15: in the packed orders those
 // are four runs of four key codes (slots 32t + 4p ..), eight runs of two value codes (slots
 // 16g + 2p ..) and eight bits of each sign word, so a lane needs a few bytes of each array and writes
-// 16 neighbouring values.  Bound by the values written.
+// 16 neighbouring values.  The lanes of a row fetch its codes in 16-byte pieces and pass them through
+// shared memory (each lane its own bytes from global memory: 27 narrow loads, 53 us for 32K tokens in 3/3
+// bits, bound by the L1's tag stage; now 44 us).  Two or three sets of rows per warp, all loads first, took
+// 46 and 53 us.  Bound by the values written and the latency of a row's chain slot -> codes -> values.
 
 struct ReadArgs {
   int N, Hkv, pages, ps, qjl;
@@ -250,53 +253,54 @@ __device__ __forceinline__ void store16(T* dst, const float (&v)[16]) {
   }
 }
 
-constexpr int RT = 256;
+// Threads of a CTA: rows leave in small portions, so that others start (32K tokens, 3/3 bits: 44 us; with 128
+// threads 45 us, with 256 48 us).
+constexpr int RT = 64;
 
 template <int KB, int VB, typename T>
 __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs a) {
   constexpr int PITCH = 16 * (KB + VB) + 16;  // packed codes of a row (the fields of four rows in different banks)
   __shared__ __align__(16) unsigned char rows[RT / 8][PITCH];
-  const uint32_t r = blockIdx.x * (uint32_t)(RT / 8) + (threadIdx.x >> 3);  // (at most 2^30 rows)
   const int p = threadIdx.x & 7;
-  const bool live = r < (uint32_t)a.N * (uint32_t)a.Hkv;
+  const uint32_t r = blockIdx.x * (uint32_t)(RT / 8) + (threadIdx.x >> 3);
+  const bool live = r < (uint32_t)a.N * (uint32_t)a.Hkv;  // (at most 2^30)
+  // the codebooks, an entry per lane: a lookup is a shuffle (so whole warps stay to the end)
+  const float kc = __ldg(a.kc + (threadIdx.x & ((1 << KB) - 1))), vc = __ldg(a.vc + (threadIdx.x & ((1 << VB) - 1)));
+  unsigned char* mine = rows[threadIdx.x >> 3];
   int64_t row = -1;
   if (live) {
     const uint32_t n = r / (uint32_t)a.Hkv;
     row = slot_row(a.slots[n], (int)(r - n * a.Hkv), a.Hkv, a.pages, a.ps);
   }
-  // the codebooks, an entry per lane: a lookup is a shuffle (so whole warps stay to the end)
-  const float kc = __ldg(a.kc + (threadIdx.x & ((1 << KB) - 1))), vc = __ldg(a.vc + (threadIdx.x & ((1 << VB) - 1)));
-  unsigned char* mine = rows[threadIdx.x >> 3];
-  uint4 sg = make_uint4(0, 0, 0, 0);
+  uint4 codes = make_uint4(0, 0, 0, 0), sg = codes;
   float kn = 0.0f, vn = 0.0f, rn = 0.0f;
   if (row >= 0) {
     if (p < KB + VB) {
       const uint8_t* src = p < KB ? a.k_codes + row * (16 * KB) + 16 * p : a.v_codes + row * (16 * VB) + 16 * (p - KB);
-      *reinterpret_cast<uint4*>(mine + 16 * p) = __ldg(reinterpret_cast<const uint4*>(src));
+      codes = __ldg(reinterpret_cast<const uint4*>(src));
     }
     if (a.signs) sg = *reinterpret_cast<const uint4*>(a.k_signs + row * 16);
     kn = a.k_norm[row] * 0.08838834764831845f;  // 1 / sqrt(128)
     vn = a.v_norm[row] * 0.08838834764831845f;
     if (a.rnorm) rn = a.k_rnorm[row];
   }
+  if (p < KB + VB) *reinterpret_cast<uint4*>(mine + 16 * p) = codes;
   __syncwarp();
-  uint32_t kq[4] = {0, 0, 0, 0}, vq[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (row >= 0) {
-    // key codes: 4 KB bits at bit KB (32t + 4p); value codes: 2 VB bits at bit VB (16g + 2p)
-    const unsigned char* kr = mine + (4 * KB * p) / 8;
-    const unsigned char* vr = mine + 16 * KB + (2 * VB * p) / 8;
-    const int ks = (4 * KB * p) & 7, vs = (2 * VB * p) & 7;
+  uint32_t kq[4], vq[8];
+  // key codes: 4 KB bits at bit KB (32t + 4p); value codes: 2 VB bits at bit VB (16g + 2p)
+  const unsigned char* kr = mine + (4 * KB * p) / 8;
+  const unsigned char* vr = mine + 16 * KB + (2 * VB * p) / 8;
+  const int ks = (4 * KB * p) & 7, vs = (2 * VB * p) & 7;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if constexpr (KB == 4) kq[t] = *reinterpret_cast<const uint16_t*>(kr + 16 * t);
-      else if constexpr (KB == 2) kq[t] = kr[8 * t];
-      else kq[t] = ((uint32_t)kr[12 * t] | (uint32_t)kr[12 * t + 1] << 8) >> ks;
-    }
+  for (int t = 0; t < 4; ++t) {
+    if constexpr (KB == 4) kq[t] = *reinterpret_cast<const uint16_t*>(kr + 16 * t);
+    else if constexpr (KB == 2) kq[t] = kr[8 * t];
+    else kq[t] = ((uint32_t)kr[12 * t] | (uint32_t)kr[12 * t + 1] << 8) >> ks;
+  }
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      if constexpr (VB == 3) vq[g] = ((uint32_t)vr[6 * g] | (uint32_t)vr[6 * g + 1] << 8) >> vs;  // (the byte behind the row: the pad)
-      else vq[g] = vr[2 * VB * g] >> vs;
-    }
+  for (int g = 0; g < 8; ++g) {
+    if constexpr (VB == 3) vq[g] = ((uint32_t)vr[6 * g] | (uint32_t)vr[6 * g + 1] << 8) >> vs;  // (inside the pad at the end)
+    else vq[g] = vr[2 * VB * g] >> vs;
   }
   float v[16];
 #pragma unroll
@@ -319,8 +323,8 @@ __global__ void __launch_bounds__(RT) read_rows(const __grid_constant__ ReadArgs
 #pragma unroll
     for (int k = 0; k < 4; ++k) {  // four rows: h = k / 2, words 2 (k % 2) and + 1, e = 0, 1
       const uint32_t x = (w[2 * (k & 1)] >> (k >> 1)) & 0x00010001u, y = (w[2 * (k & 1) + 1] >> (k >> 1)) & 0x00010001u;
-      const uint32_t v = __byte_perm(x, y, 0x6420);
-      o[k] = row >= 0 ? v | ((v ^ 0x01010101u) * 255u) : 0u;
+      const uint32_t b = __byte_perm(x, y, 0x6420);
+      o[k] = row >= 0 ? b | ((b ^ 0x01010101u) * 255u) : 0u;
     }
     reinterpret_cast<uint4*>(a.signs)[(int64_t)r * 8 + p] = make_uint4(o[0], o[1], o[2], o[3]);
   }
