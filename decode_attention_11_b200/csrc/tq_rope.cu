@@ -13,7 +13,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cmath>
 
 #include "tq_internal.h"
@@ -23,15 +22,13 @@ namespace {
 
 constexpr int D = kHeadDim;
 constexpr int PAIRS = D / 2;
-constexpr int TOK = 4;       // tokens of a CTA
-constexpr int PRE = 5;       // heads a thread has loads in flight for
+constexpr int PRE = 3;       // heads a thread has loads in flight for
 
 struct RopeArgs {
   const void* x[2];          // q, k
   void* y[2];
   int64_t sn[2], sh[2];      // input strides (elements)
   int H[2];
-  int N;
   const int32_t* pos;
   int64_t pos_stride;
   float sign;                // -1: inverse
@@ -78,15 +75,16 @@ struct Vec<float> {
 };
 
 // V threads share a head: thread c works on its pairs c E .. c E + E - 1: the 16-byte vectors c and c + V
-// (HALF), or 2c and 2c + 1 (PAIR).  A CTA has T tokens, 64 threads each.
-template <typename T, bool HALF, int TK>
-__global__ void __launch_bounds__(PAIRS * TK) rope_kernel(const __grid_constant__ RopeArgs a) {
+// (HALF), or 2c and 2c + 1 (PAIR).  A CTA has one token: four to a CTA took 56 us for 16384 tokens of 40 bf16
+// heads where this takes 52 us, and loads for five heads in flight 19.0 us for 5003 tokens of 18 fp32 heads
+// where those for three take 18.1 us (fewer registers, more CTAs).
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(PAIRS) rope_kernel(const __grid_constant__ RopeArgs a) {
   using Vc = Vec<T>;
   constexpr int E = Vc::N, V = PAIRS / E, HS = PAIRS / V;  // HS: heads at a time
-  __shared__ __align__(16) float2 cs[TK][PAIRS];
-  const int tok = threadIdx.x / PAIRS, i64 = threadIdx.x % PAIRS, c = i64 % V, h0 = i64 / V;
-  const int n = blockIdx.x * TK + tok;
-  const int H = n < a.N ? a.H[0] + a.H[1] : 0;
+  __shared__ __align__(16) float2 cs[PAIRS];
+  const int i64 = threadIdx.x, c = i64 % V, h0 = i64 / V;
+  const int n = blockIdx.x, H = a.H[0] + a.H[1];
   constexpr int STEP = HALF ? V : 1;
   const int first = HALF ? c : 2 * c;
   const T* in[2] = {reinterpret_cast<const T*>(a.x[0]) + (int64_t)n * a.sn[0], reinterpret_cast<const T*>(a.x[1]) + (int64_t)n * a.sn[1]};
@@ -100,17 +98,15 @@ __global__ void __launch_bounds__(PAIRS * TK) rope_kernel(const __grid_constant_
 #pragma unroll
   for (int p = 0; p < PRE; ++p)
     if (h0 + p * HS < H) load(p, h0 + p * HS);
-  if (n < a.N) {
-    const double t = (double)a.pos[a.axis[i64] * a.pos_stride + n] * a.turns[i64];
-    float s, co;
-    sincospif(2.0f * (float)(t - rint(t)), &s, &co);
-    cs[tok][i64] = make_float2(co, a.sign * s);
-  }
+  const double t = (double)a.pos[a.axis[i64] * a.pos_stride + n] * a.turns[i64];
+  float s, co;
+  sincospif(2.0f * (float)(t - rint(t)), &s, &co);
+  cs[i64] = make_float2(co, a.sign * s);
   __syncthreads();
   float2 w[E];
 #pragma unroll
   for (int i = 0; i < E; i += 2) {
-    const float4 v = *reinterpret_cast<const float4*>(&cs[tok][c * E + i]);
+    const float4 v = *reinterpret_cast<const float4*>(&cs[c * E + i]);
     w[i] = make_float2(v.x, v.y);
     w[i + 1] = make_float2(v.z, v.w);
   }
@@ -137,13 +133,6 @@ __global__ void __launch_bounds__(PAIRS * TK) rope_kernel(const __grid_constant_
       if (h + PRE * HS < H) load(p, h + PRE * HS);
     }
   }
-}
-
-template <typename T, bool HALF>
-void launch_rope(const RopeArgs& a, int sms, cudaStream_t s) {
-  // one token per CTA while those do not fill the SMs' CTA slots
-  if (a.N <= 8 * sms) rope_kernel<T, HALF, 1><<<a.N, PAIRS, 0, s>>>(a);
-  else rope_kernel<T, HALF, TOK><<<(a.N + TOK - 1) / TOK, PAIRS * TOK, 0, s>>>(a);
 }
 
 // base^(-2i/128) / (2 pi) for all pairs: six square roots and products of their powers in extended
@@ -208,20 +197,16 @@ extern "C" tq_status tq_rope(const void* q, int64_t q_stride_n, int64_t q_stride
     a.sh[w] = sh[w];
     a.H[w] = H[w];
   }
-  a.N = N;
   a.pos = pos;
   a.pos_stride = pos_stride;
   a.sign = inverse ? -1.0f : 1.0f;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    cudaGetLastError();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == TQ_BF16) {
-    if (style == TQ_ROPE_HALF) launch_rope<__nv_bfloat16, true>(a, sms, s);
-    else launch_rope<__nv_bfloat16, false>(a, sms, s);
+    if (style == TQ_ROPE_HALF) rope_kernel<__nv_bfloat16, true><<<N, PAIRS, 0, s>>>(a);
+    else rope_kernel<__nv_bfloat16, false><<<N, PAIRS, 0, s>>>(a);
   } else {
-    if (style == TQ_ROPE_HALF) launch_rope<float, true>(a, sms, s);
-    else launch_rope<float, false>(a, sms, s);
+    if (style == TQ_ROPE_HALF) rope_kernel<float, true><<<N, PAIRS, 0, s>>>(a);
+    else rope_kernel<float, false><<<N, PAIRS, 0, s>>>(a);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
