@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ Prep
 // ------------------------------------------------------------------------------------------ merge
 //
 // HPW heads per warp: a CTA joins the partials of 8 HPW heads and turns the joined o' back,
-// o_i = sum_j Pi[j][i] o'_j.  HPW = 0, for too few
-// heads to fill the SMs: one head, whose partials the eight warps share.
+// o_i = sum_j Pi[j][i] o'_j.  HPW = 0, for too few heads to fill the SMs: one head, whose partials the
+// eight warps share.  Two CTAs share an SM (128 registers: ten more cost a batch of 512 heads 4 us).
 
 struct MergeArgs {
   int B, Hkv, g, hgroups, hgn, ctas, warps, units;
@@ -390,7 +390,7 @@ struct Records {
 };
 
 template <int HPW>
-__global__ void __launch_bounds__(MT) paged_merge(const __grid_constant__ MergeArgs a) {
+__global__ void __launch_bounds__(MT, 2) paged_merge(const __grid_constant__ MergeArgs a) {
   constexpr bool ONE = HPW == 0;
   constexpr int R = ONE ? 8 : 8 * HPW;
   __shared__ __align__(16) Vecs<R> vec;
