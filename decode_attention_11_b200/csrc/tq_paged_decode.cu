@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(MT, 1) paged_prep(const __grid_constant__ Prep
 
 // ------------------------------------------------------------------------------------------ merge
 //
-// HPW heads per warp: a CTA joins the partials of 8 HPW heads and turns the joined o' back,
-// o_i = sum_j Pi[j][i] o'_j.  HPW = 0, for too few heads to fill the SMs: one head, whose partials the
-// eight warps share.  Two CTAs share an SM (128 registers: ten more cost a batch of 512 heads 4 us).
+// A CTA joins the partials of eight heads, one per warp, and turns the joined o' back,
+// o_i = sum_j Pi[j][i] o'_j.  ONE, for few heads: one head, whose partials the eight warps share.  Two CTAs
+// share an SM (128 registers: ten more cost a batch of 512 heads 4 us).
 
 struct MergeArgs {
   int B, Hkv, g, hgroups, hgn, ctas, warps, units;
@@ -389,10 +389,9 @@ struct Records {
   }
 };
 
-template <int HPW>
+template <bool ONE>
 __global__ void __launch_bounds__(MT, 2) paged_merge(const __grid_constant__ MergeArgs a) {
-  constexpr bool ONE = HPW == 0;
-  constexpr int R = ONE ? 8 : 8 * HPW;
+  constexpr int R = 8;
   __shared__ __align__(16) Vecs<R> vec;
   __shared__ __align__(16) float res[R][VS];
   __shared__ float rm[MW], rl[MW];
@@ -409,9 +408,8 @@ __global__ void __launch_bounds__(MT, 2) paged_merge(const __grid_constant__ Mer
   constexpr int STEP = ONE ? 1 : R;
   for (int p0 = blockIdx.x * STEP; p0 < heads; p0 += gridDim.x * STEP) {
     if (ONE && !head_place(p0, a.hgn, a.hgroups, a.g, a.units).live) continue;
-#pragma unroll
-    for (int x = 0; x < (ONE ? 1 : HPW); ++x) {
-      const HeadPlace h = head_place(ONE ? p0 : p0 + HPW * warp + x, a.hgn, a.hgroups, a.g, a.units);
+    {
+      const HeadPlace h = head_place(ONE ? p0 : p0 + warp, a.hgn, a.hgroups, a.g, a.units);
       float M = -1e30f, L = 0.0f;
       float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       int S = 0;
@@ -483,18 +481,16 @@ __global__ void __launch_bounds__(MT, 2) paged_merge(const __grid_constant__ Mer
       }
       if (!ONE || warp == 0) {
         const float inv = L != 0.0f ? 1.0f / L : 0.0f;
-        vec.put(ONE ? 0 : HPW * warp + x, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+        vec.put(ONE ? 0 : warp, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
         if (h.live && a.lse && lane == 0) a.lse[h.row] = S ? M * 0.69314718055994531f + logf(L) : -INFINITY;
       }
     }
     __syncthreads();
     product(pt, vec, res, warp, gq, t);
     __syncthreads();
-#pragma unroll
-    for (int x = 0; x < (ONE ? 1 : HPW); ++x) {
-      const int r = ONE ? 0 : HPW * warp + x;
-      const HeadPlace h = head_place(p0 + r, a.hgn, a.hgroups, a.g, a.units);
-      if (!h.live || (ONE && warp)) continue;
+    const int r = ONE ? 0 : warp;
+    const HeadPlace h = head_place(p0 + r, a.hgn, a.hgroups, a.g, a.units);
+    if (h.live && !(ONE && warp)) {
       const float4 v = *reinterpret_cast<const float4*>(&res[r][4 * lane]);
       if (a.out_bf16) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -683,10 +679,10 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   m.out_bf16 = out_dtype == TQ_BF16;
   m.lse = lse;
   m.units = (int)w.units;
-  // Sixteen heads at a time when that gives every CTA (two fit an SM) a round, eight while that fills half
-  // the SMs' CTAs, else one.
+  // One head per CTA while all fit at once (two CTAs per SM), else eight: 256 heads of 512 tokens 22 against
+  // 25 us, 384 heads 26 against 25.5, 1024 heads 35 against 26, 9600 heads 147 against 61.  (Sixteen at a
+  // time were no faster than eight anywhere, and 4 to 6 us slower up to 1200 heads.)
   const int64_t heads = w.units * m.hgn, room = 2 * sms;
-  if (heads >= 16 * room) return launch_dep(paged_merge<2>, room, MT, s, true, "paged merge", m);
-  if (heads >= 4 * room) return launch_dep(paged_merge<1>, std::min<int64_t>(heads / 8, room), MT, s, true, "paged merge", m);
-  return launch_dep(paged_merge<0>, std::min<int64_t>(heads, room), MT, s, true, "paged merge", m);
+  if (heads <= room) return launch_dep(paged_merge<true>, heads, MT, s, true, "paged merge", m);
+  return launch_dep(paged_merge<false>, std::min<int64_t>((heads + MW - 1) / MW, room), MT, s, true, "paged merge", m);
 }

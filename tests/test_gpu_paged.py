@@ -160,7 +160,7 @@ def test_decode_long_and_many(B, Hkv, Hq, lens):
 
 @pytest.mark.parametrize("B,Hkv,Hq,window", [(600, 2, 8, 0), (520, 2, 10, 9)])
 def test_decode_large_batches(B, Hkv, Hq, window):
-    """More sequences than a CTA keeps lengths of (512), and enough heads for the merge kernel's widest form;
+    """More sequences than a CTA keeps lengths of (512), and more heads than the merge kernel takes in one round;
     one sequence in three is empty."""
     ps = 16
     r = np.random.RandomState(B)
