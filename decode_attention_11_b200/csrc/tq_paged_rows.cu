@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(QT, 1) quantize_rows(const __grid_constant__ R
 // 16g + 2p ..) and eight bits of each sign word, so a lane needs a few bytes of each array and writes
 // 16 neighbouring values.  The lanes of a row fetch its codes in 16-byte pieces and pass them through
 // shared memory (each lane its own bytes from global memory: 27 narrow loads, 53 us for 32K tokens in 3/3
-// bits, bound by the L1's tag stage; now 44 us).  Two or three sets of rows per warp, all loads first, took
+// bits, bound by the L1's tag stage; now 41 us).  Two or three sets of rows per warp, all loads first, took
 // 46 and 53 us.  Bound by the values written and the latency of a row's chain slot -> codes -> values.
 
 struct ReadArgs {
@@ -253,8 +253,8 @@ __device__ __forceinline__ void store16(T* dst, const float (&v)[16]) {
   }
 }
 
-// Threads of a CTA: rows leave in small portions, so that others start (32K tokens, 3/3 bits: 44 us; with 128
-// threads 45 us, with 256 48 us).
+// Threads of a CTA: rows leave in small portions, so that others start (32K tokens, 3/3 bits, 64, 128 and
+// 256 threads: 44, 45 and 48 us with pages in random order).
 constexpr int RT = 64;
 
 template <int KB, int VB, typename T>
