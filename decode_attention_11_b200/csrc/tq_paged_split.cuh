@@ -27,8 +27,11 @@
 // The 8 columns of B are four heads, hi and lo side by side (one product), or, for five to eight heads,
 // eight heads, hi and lo in two products onto the same sums: that keeps the sums at 32 registers.  The
 // running maximum moves only when a score passes it by more than LAZY (a vote instead of a three-step
-// exchange per group), so exp reaches 2^LAZY.  The weights carry a power of two that brings them into
-// fp16 range whatever the values' norms are; it moves, by the same vote, when a norm outgrows it.
+// exchange per group), so exp reaches 2^LAZY.  The weights exp * norm of a head carry a scale that brings
+// them into fp16 range.  It is set from the weights themselves (set from the norms alone, a large norm at a
+// score far below the maximum would push the weights that count into fp16's subnormals, and past 2^36 times
+// the other norms to zero), by the same vote: when the maximum moves, and when a norm could carry a weight
+// past the range.
 // Rows outside the tokens shown are masked by selection, never by a product, so whatever they hold
 // (NaN too) stays out.
 #pragma once
@@ -42,10 +45,13 @@ namespace tq {
 namespace {
 
 constexpr float LAZY = 4.0f;
-// exponent of the largest value norm times its scale when that is set, and the bound at which it is set
-// anew: times 2^LAZY that stays below fp16's 65504
-constexpr int NORM_EXP = 8;
-constexpr float NORM_LIMIT = 2048.0f;
+// Weights in fp16: the largest of a group is brought into [2^W_EXP, 2^(W_EXP + 1)) when a head's scale is
+// set (hi + lo then leaves 2^-31 of it), and the scale is looked at again when a norm times it passes W_LIMIT:
+// times 2^LAZY that stays below fp16's 65504.  With W_EXP = 8 ordinary norms passed the limit so often that
+// 64 sequences to 16K in 3/2 bits took 131 us, with 6 they take 125 us.
+constexpr int W_EXP = 6;
+constexpr float W_LIMIT = 2048.0f;
+constexpr float W_START = 0x1p120f;         // scale of a segment without sums: any weight sets it anew
 constexpr int P_LENS = 512;                 // sequences whose lengths and running sums are kept in shared memory
 constexpr int P_SMEM = 232448;              // dynamic shared memory of a CTA (all an SM gives one)
 constexpr int P_MISC = 8192;                // lengths, sums, codebooks
@@ -395,8 +401,7 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
   // Sums of the values: dim block db: dims 16db + gq (columns 2t, 2t + 1 in [0], [1]) and 16db + 8 + gq
   // ([2], [3]).
   float oacc[8][4];
-  float m_run[H], l_run[H];
-  float vscale = 1.0f, vlimit = -1.0f;  // weights are exp * norm * vscale; the largest norm that fits
+  float m_run[H], l_run[H], vscale[H];  // weights are exp * norm * vscale
   while (left > 0) {
     const int64_t unit = (int64_t)cur.b * U + cur.uu;
     const bool opens = cur.gi == 0;
@@ -436,9 +441,8 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
     for (int x = 0; x < H; ++x) {
       m_run[x] = -1e30f;  // finite: ex2(s - m) and ex2(m_old - m_new) never see inf - inf
       l_run[x] = 0.0f;
+      vscale[x] = W_START;
     }
-    vscale = 1.0f;
-    vlimit = -1.0f;  // (the first group sets them)
     int tk = kGroup * (cur.first / kGroup + cur.gi) + gq - cur.first;  // row gq's place among the tokens shown
     const uint32_t shown = (uint32_t)(cur.len - cur.first);
     for (; n > 0; --n, tk += kGroup) {
@@ -496,7 +500,8 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
       }
       const float nv0 = v0ok ? ldf<64>(np) : 0.0f, nv1 = v1ok ? ldf<96>(np) : 0.0f;
       float sc0[H], sc1[H];  // scores of the two tokens
-      bool over = fmaxf(nv0, nv1) > vlimit;
+      const float nv = fmaxf(nv0, nv1);
+      bool over = false;
 #pragma unroll
       for (int x = 0; x < H; ++x) {
         // a head's sum: its columns hi + lo, or its column of the blocks hi + lo
@@ -511,43 +516,37 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
         }
         sc0[x] = v0ok ? s0v : -INFINITY;
         sc1[x] = v1ok ? s1v : -INFINITY;
-        over = over || fmaxf(sc0[x], sc1[x]) > m_run[x] + LAZY;
+        over = over || fmaxf(sc0[x], sc1[x]) > m_run[x] + LAZY || nv * vscale[x] > W_LIMIT;
       }
-      if (__any_sync(FULL, over)) {  // the running maximum of some head moves, or the norms' scale
-        float nm = fmaxf(nv0, nv1);
-        nm = fmaxf(nm, __shfl_xor_sync(FULL, nm, 4));
-        nm = fmaxf(nm, __shfl_xor_sync(FULL, nm, 8));
-        nm = fmaxf(nm, __shfl_xor_sync(FULL, nm, 16));
-        if (nm > vlimit) {  // warp-uniform
-          const int e = max(((__float_as_int(nm) >> 23) & 255) - 127, -100);
-          const float now = __int_as_float((127 + NORM_EXP - e) << 23);
-          const float r = vlimit < 0.0f ? 0.0f : now / vscale;  // (nothing has been summed yet)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) oacc[i][j] *= r;
-          vscale = now;
-          vlimit = NORM_LIMIT / now;
-        }
+      if (__any_sync(FULL, over)) {  // the running maximum of some head moves, or its weights' scale
 #pragma unroll
         for (int x = 0; x < H; ++x) {
-          float mx = fmaxf(sc0[x], sc1[x]);
-          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-          mx = fmaxf(mx, m_run[x]);
-          const float alpha = ex2(m_run[x] - mx);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            oacc[i][x] *= alpha;
-            oacc[i][2 + x] *= alpha;
-            if constexpr (NB == 1) {
-              oacc[i][1] *= alpha;
-              oacc[i][3] *= alpha;
-            }
-          }
+          auto top = [](float v) {  // over the 16 tokens
+            v = fmaxf(v, __shfl_xor_sync(FULL, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(FULL, v, 8));
+            return fmaxf(v, __shfl_xor_sync(FULL, v, 16));
+          };
+          const float mx = fmaxf(top(fmaxf(sc0[x], sc1[x])), m_run[x]);
+          const float alpha = ex2(m_run[x] - mx), grow = ex2(mx - m_run[x]);
           l_run[x] *= alpha;
           m_run[x] = mx;
+          // The new scale is the one for this group's weights, or the one at which the sums so far stay as
+          // they are (their weights fitted), whichever is smaller.
+          const float w = top(fmaxf(ex2(sc0[x] - mx) * nv0, ex2(sc1[x] - mx) * nv1));
+          const int ex = max(((__float_as_int(w) >> 23) & 255) - 127, -100);
+          const float fresh = __int_as_float((127 + W_EXP - ex) << 23);
+          const float scale = fminf(fresh, vscale[x] * grow);  // (grow is infinite where alpha is 0)
+          const float r = __fdividef(alpha * scale, vscale[x]);
+          vscale[x] = scale;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            oacc[i][x] *= r;
+            oacc[i][2 + x] *= r;
+            if constexpr (NB == 1) {
+              oacc[i][1] *= r;
+              oacc[i][3] *= r;
+            }
+          }
         }
       }
       // weights as fp16 hi and lo, turned from (token row, columns 2t, 2t + 1) into (column gq, tokens 2t,
@@ -560,8 +559,8 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
           const float e0 = ex2(sc0[x] - m_run[x]);  // ex2(-inf) = 0 for rows that are not shown
           const float e1 = ex2(sc1[x] - m_run[x]);
           l_run[x] += e0 + e1;
-          p0[x] = e0 * (nv0 * vscale);
-          p1[x] = e1 * (nv1 * vscale);
+          p0[x] = e0 * (nv0 * vscale[x]);
+          p1[x] = e1 * (nv1 * vscale[x]);
         }
         if constexpr (NB == 1) {
           bp[0][0] = movmatrix_trans(hilo_half2(p0[0]));
@@ -637,11 +636,12 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
       l_run[x] += __shfl_xor_sync(FULL, l_run[x], 8);
       l_run[x] += __shfl_xor_sync(FULL, l_run[x], 16);
     }
-    const float vback = 0.08838834764831845f / vscale;  // with the values' 1 / sqrt(128)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int j = 0; j < 4; ++j) {
+      const float vback = 0.08838834764831845f / vscale[NB == 1 ? 0 : j & (H - 1)];  // with the values' 1 / sqrt(128)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) oacc[i][j] *= vback;
+      for (int i = 0; i < 8; ++i) oacc[i][j] *= vback;
+    }
     if (joint) break;  // (the range's only segment)
 #pragma unroll
     for (int x = 0; x < H; ++x) {

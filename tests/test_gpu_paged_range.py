@@ -1,0 +1,76 @@
+"""Paged decode attention where single tokens are far out of scale, against the float64 oracle.
+
+Output tolerance where one token has all the weight.  Its weight enters as fp16 hi + lo (2^-22) and its
+values are exact; sums and normalisation are fewer than 16 fp32 roundings (16 * 2^-24).  The rotation back
+drops products of two lo parts and rounds the parts (2^-21 of each product) and sums eight k-steps in fp32
+(24 * 2^-24 at most): a coordinate is off by that times sum_j |Pi[j][i]| |o'[j]| <= |o'|, so the vector by
+sqrt(128) (2^-21 + 24 * 2^-24) = 2.2e-5 of its norm.  Together below 3e-5.
+
+lse: a score's error is at most |q| |k| / sqrt(128) * (2 * 2^-22 + 24 * 2^-23) (q' and S q' as hi + lo, 24
+fp32 sums)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import decode_attention_11_b200 as tq
+from oracle import tq_oracle as O
+
+from test_gpu_paged import PI, S, filled_pool, params, reference, rows_of, table_for
+
+pytestmark = pytest.mark.gpu
+
+ALL_WEIGHT = 3e-5
+SCORE = 2 * 2.0**-22 + 24 * 2.0**-23
+
+
+def like_queries(B, Hq, seed=5):
+    """Queries of norm 15 whose heads differ little, so that one key stands out for all of them."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn(B, 1, 128, generator=g, device="cuda") + 0.05 * torch.randn(B, Hq, 128, generator=g, device="cuda")
+    return q * (15.0 / q.norm(dim=-1, keepdim=True))
+
+
+def raise_score(pool, table, q, b, lo, hi, score):
+    """The token of [lo, hi) that suits sequence b's queries best gets the key norm that gives head 0 that score."""
+    t = np.arange(lo, hi)
+    c = rows_of(pool, table, b, t)
+    est = O.score_estimates(q[b, 0].double().cpu().numpy(), PI, S, c["k_codes"][0, 0], c["k_norm"][0, 0], pool.k_bits,
+                            c["k_signs"][0, 0], c["k_rnorm"][0, 0]) / math.sqrt(128)
+    i = int(np.argmax(est / c["k_norm"][0, 0]))
+    norm = float(c["k_norm"][0, 0, i] * score / est[i])
+    page, off = table[b, t[i] // pool.T_cap].long(), int(t[i]) % pool.T_cap
+    pool.k_norm[page, 0, off], pool.k_rnorm[page, 0, off] = norm, 0.15 * norm
+    return int(t[i]), norm
+
+
+@pytest.mark.parametrize("Hq", [3, 6])
+@pytest.mark.parametrize("kb,vb", [(4, 4), (3, 2)])
+@pytest.mark.parametrize("ratio", [2.0**20, 2.0**30, 2.0**36])
+def test_large_value_norm_without_weight(Hq, kb, vb, ratio):
+    """A token whose value norm is 2^20 .. 2^36 times the others', at a score about 60 below the maximum (it
+    adds less than 1e-14), before and after the token that has the weight, in its group of 16 and in the
+    groups beside it (a warp's range is three to five groups here)."""
+    away = [1, -1, 3, -3, 7, -7, 16, -16, 20, -20, 33, -33]
+    B, ps, T = len(away), 64, 8000
+    lens = [T] * B
+    pages = B * (-(-T // ps))
+    pool = filled_pool(pages, 1, ps, kb, vb, seed=kb)
+    pool.k_norm.mul_(0.1)  # scores of a few units
+    pool.k_rnorm.mul_(0.1)
+    table = table_for(lens, ps, pages)
+    q = like_queries(B, Hq)
+    norms = []
+    for b, d in enumerate(away):
+        i, n = raise_score(pool, table, q, b, 4000 + 64 * b, 4064 + 64 * b, 60.0)
+        norms.append(n)
+        pool.v_norm[table[b, (i + d) // ps].long(), 0, (i + d) % ps] = 10.0 * ratio
+    out, lse = tq.paged_decode_attn(params(kb, vb), q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    ref, rl = reference(q, pool, table, lens)
+    got = out.double().cpu().numpy()
+    err = np.linalg.norm(got - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert (err <= ALL_WEIGHT).all(), err.max(axis=1)
+    tol = 15.0 * np.array(norms)[:, None] / math.sqrt(128) * SCORE + 2.0**-22 * np.abs(rl)
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= tol).all()
