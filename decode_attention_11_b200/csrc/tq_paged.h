@@ -12,6 +12,10 @@ namespace tq {
 
 constexpr int kGroup = kPageTokens;  // tokens of a group: the unit of work, inside one page
 
+// Running maximum before any score.  Finite, so that differences of maxima are never inf - inf, and not above
+// any finite score (at -1e30 a head whose scores were all below that came out as 0).
+constexpr float kNoScore = -3.40282347e38f;
+
 // Warps of a split CTA: multiples of four, so that its schedulers are loaded alike.  Up to four heads per
 // unit (nb = 1): 12 warps of 168 registers (128K x 4 in 4 bits: 165 us; 8 or 16 warps 185 us, 13 to 15 190 to
 // 215 us).  Up to eight: 8 warps of 232 (64 sequences to 16K, 3/2 bits: 121 us; 12 warps 127 us, 4 warps

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(MT, 2) paged_merge(const __grid_constant__ Mer
     if (ONE && !head_place(p0, a.hgn, a.hgroups, a.g, a.units).live) continue;
     {
       const HeadPlace h = head_place(ONE ? p0 : p0 + warp, a.hgn, a.hgroups, a.g, a.units);
-      float M = -1e30f, L = 0.0f;
+      float M = kNoScore, L = 0.0f;
       float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       int S = 0;
       if (h.live) {
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(MT, 2) paged_merge(const __grid_constant__ Mer
           float top = M;
 #pragma unroll
           for (int i = 0; i < BATCH; ++i) {
-            if (s0 + i * NEXT >= S) ml[i] = make_float2(-1e30f, 0.0f);
+            if (s0 + i * NEXT >= S) ml[i] = make_float2(kNoScore, 0.0f);
             top = fmaxf(top, ml[i].x);
           }
           const float w0 = ex2(M - top);

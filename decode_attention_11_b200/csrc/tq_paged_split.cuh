@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
     for (int i = 0; i < 8; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.0f;
 #pragma unroll
     for (int x = 0; x < H; ++x) {
-      m_run[x] = -1e30f;  // finite: ex2(s - m) and ex2(m_old - m_new) never see inf - inf
+      m_run[x] = kNoScore;
       l_run[x] = 0.0f;
       vscale[x] = W_START;
     }
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
         const uint32_t r = w < front ? base + w * (DEPTH * SLOT) : tbl + Lay::TBL_BYTES + (w - front) * (DEPTH * SLOT);
         return reinterpret_cast<const float*>(smem + (r - base));
       };
-      float M = -1e30f, Ls = 0.0f, O = 0.0f;
+      float M = kNoScore, Ls = 0.0f, O = 0.0f;
       for (int w = 0; w < cut.warps; ++w) M = fmaxf(M, of(w)[2 * i]);
       for (int w = 0; w < cut.warps; ++w) {
         const float* v = of(w);

@@ -264,6 +264,7 @@ size_t tq_decode_workspace_size(int B, int Hq, const tq_cache* cache, int seq_le
  *   workspace   device buffer of at least tq_decode_workspace_size() bytes, contents ignored
  * est_i = <Pi q, (n_i/sqrt(d)) c_K[idx_i]> + ||r_i|| sqrt(pi/2)/m <S Pi q, 2 sign_i - 1>,
  * vhat'_i = (nV_i/sqrt(d)) c_V[idxV_i]  (rotated basis).
+ * A head whose scores are all below -6.9e29 gets zeros.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA.
  */
 tq_status tq_decode_attn(const tq_params* params, const void* q, int q_dtype, int Hq,
@@ -509,6 +510,7 @@ size_t tq_paged_decode_workspace_size(int B, int Hq, const tq_cache* pool);
  * A page number outside the pool (in a page that a length reaches) or a length outside
  * [0, max_pages * page_size] records bit 4 in tq_decode_device_errors; that sequence's output is then
  * not valid, the others are.  Rows past a sequence's length are never used, whatever they hold.
+ * Scores may have any size that fp32 holds; value norms up to 1e30.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_WORKSPACE, TQ_ERR_CUDA.
  */
 tq_status tq_paged_decode_attn(const tq_params* params, const void* q, int q_dtype, int B, int Hq,

@@ -74,3 +74,29 @@ def test_large_value_norm_without_weight(Hq, kb, vb, ratio):
     assert (err <= ALL_WEIGHT).all(), err.max(axis=1)
     tol = 15.0 * np.array(norms)[:, None] / math.sqrt(128) * SCORE + 2.0**-22 * np.abs(rl)
     assert (np.abs(lse.double().cpu().numpy() - rl) <= tol).all()
+
+
+@pytest.mark.parametrize("Hq", [4, 8])
+@pytest.mark.parametrize("big", [1e28, 1e31, 1e33])
+def test_scores_far_below_zero(Hq, big):
+    """Scores of +-1e28 .. +-1e33 and more: where all of a head are negative the nearest to zero has the weight,
+    and a sequence of one token gives that token whatever its score.  Half the heads are the others' negatives,
+    so both signs are there.  (Scores of two tokens that come within their error of each other are left out: the
+    fixed inputs have none.)"""
+    ps, lens = 16, [1, 1, 5, 40, 1, 0]
+    pages = sum(-(-n // ps) for n in lens)
+    pool = filled_pool(pages, 1, ps, 4, 4, seed=2)
+    table = table_for(lens, ps, pages)
+    q = like_queries(len(lens), Hq) * big
+    q[:, Hq // 2:] *= -1
+    out, lse = tq.paged_decode_attn(params(4, 4), q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    ref, rl = reference(q, pool, table, lens)
+    f = np.isfinite(rl)
+    assert (rl[f] < -1e28).any() and (rl[f] > 1e28).any()
+    err = np.linalg.norm(out.double().cpu().numpy() - ref, axis=-1)
+    assert (err <= ALL_WEIGHT * np.linalg.norm(ref, axis=-1)).all(), err
+    l = lse.double().cpu().numpy()
+    assert np.array_equal(np.isfinite(l), f) and (l[~f] == -np.inf).all()
+    # a score's error, with key norms below 29; the product with ln 2 adds two roundings of the value
+    assert (np.abs(l[f] - rl[f]) <= 15.0 * big * 29.0 / math.sqrt(128) * SCORE + 2.0**-22 * np.abs(rl[f])).all()
