@@ -163,11 +163,18 @@ class PageTable:
         return _PageTable(self.table.shape[0], self.table.shape[1], self.refs.shape[0], self.page_size,
                           self.table.data_ptr(), self.seq_lens.data_ptr(), self.refs.data_ptr(), self.status.data_ptr())
 
+    def _wait(self) -> None:
+        if self.status.is_cuda:
+            torch.cuda.synchronize(self.status.device)
+
     def check(self) -> None:
-        """Wait for the device; raise ValueError if a call on this table recorded an error, and clear it."""
+        """Wait for the device (all its streams); raise ValueError if a call on this table recorded an error,
+        and clear it."""
+        self._wait()
         bits = int(self.status.item())
         if bits:
             self.status.zero_()
+            self._wait()  # a call on another stream must not record before the clearing
             raise ValueError("page table: " + "; ".join(t for b, t in _STATUS.items() if bits & b))
 
 
