@@ -95,6 +95,27 @@ def _rope_arg(x: Optional[torch.Tensor], out: Optional[torch.Tensor], name: str,
     return (x.data_ptr(), sn, sh, H), out, out.data_ptr()
 
 
+class _Rope(torch.autograd.Function):
+    """rope for inputs that require a gradient: the turn is orthogonal, so the gradient turns back."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, sections, base, style, inverse, axis_of_pair, stream):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(pos)
+        ctx.how = sections, base, style, not inverse, axis_of_pair
+        return rope(q, k, pos, sections, base, style, inverse, axis_of_pair, stream=stream)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        pos, = ctx.saved_tensors
+        # (gradients come in any strides, a sum's with stride 0)
+        g = [x.contiguous() if x is not None and need else None for x, need in zip(grads, ctx.needs_input_grad)]
+        g = [x.clone() if x is not None and x.data_ptr() % 16 else x for x in g]
+        if g[0] is not None or g[1] is not None:
+            g = rope(*g, pos, *ctx.how)
+        return (*g, None, None, None, None, None, None, None)
+
+
 def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor, sections: Sequence[int] = (64,),
          base: float = 10000.0, style: int = TQ_ROPE_HALF, inverse: bool = False,
          axis_of_pair: Optional[Sequence[int]] = None, q_out: Optional[torch.Tensor] = None,
@@ -104,10 +125,15 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos: torch.Tensor
     pos: int32 [N], or [axes, N] with one row per axis; sections: how many of the 64 pairs follow each
     axis, in order (or axis_of_pair: the axis of each pair).  inverse=True turns back, and is the
     gradient: d(rope(x))/dx applied to g is rope(g, inverse=True).  Returns (q_out, k_out); q_out = q
-    works in place for a contiguous q."""
+    works in place for a contiguous q.  Autograd follows it (not into q_out or k_out)."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
+    if torch.is_grad_enabled() and (x.requires_grad or (k is not None and k.requires_grad)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out / k_out given for an input that requires a gradient")
+        return _Rope.apply(q, k, pos, tuple(sections), base, style, inverse,
+                           None if axis_of_pair is None else bytes(axis_of_pair), stream)
     device, N, n_axes, pos_stride = x.device, x.shape[0], 1, 0
     if pos.dim() == 2:
         n_axes, n = pos.shape
