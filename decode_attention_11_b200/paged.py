@@ -31,6 +31,9 @@ _STATUS = {TQ_PAGES_NO_ROOM: "not enough free pages", TQ_PAGES_BAD_INDEX: "a num
            TQ_PAGES_SHARED: "growth inside a shared page"}
 
 
+_INT_MAX = 0x7fffffff  # (ctypes cuts an int to 32 bits without a word; no sequence is longer)
+
+
 def _elsewhere(device: torch.device, stream) -> bool:
     """Whether the tensors' device or the call's stream is not the current one.  Such a call is made again
     under `_on`, so that what it allocates belongs to that stream; the usual call pays for one test."""
@@ -381,6 +384,6 @@ def paged_decode_attn(params: Params, q: torch.Tensor, pool: Cache, table: torch
                                 device=device)
     _check(lib().tq_paged_decode_attn(
         ctypes.byref(p), q.data_ptr(), _dtype_code(q), B, Hq, ctypes.byref(c), table.data_ptr(),
-        table_stride if B > 1 else max(table_stride, max_pages), max_pages, seq_lens.data_ptr(), window, scale, out.data_ptr(),
+        table_stride if B > 1 else max(table_stride, max_pages), max_pages, seq_lens.data_ptr(), max(-1, min(window, _INT_MAX)), scale, out.data_ptr(),
         _dtype_code(out), _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(device)))
     return (out, lse) if return_lse else out

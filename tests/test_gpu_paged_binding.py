@@ -134,3 +134,25 @@ def test_rope_gradient_forms():
     pos.add_(1)
     with pytest.raises(RuntimeError):
         out.sum().backward()
+
+
+# -------------------------------------------------------------------------- numbers past 32 bits
+
+def test_window_past_32_bits_sees_all():
+    """A window wider than any sequence shows all tokens, also where its low 32 bits say something else."""
+    pool = tq.Cache.allocate(4, 1, 16, 4, 4, 0)
+    for n in ("k_codes", "v_codes"):
+        getattr(pool, n).random_(0, 256)
+    pool.k_norm.fill_(3.0)
+    pool.v_norm.fill_(3.0)
+    p = tq.Params.create(torch.eye(128).numpy(), None, 4, 4)
+    q = torch.randn(1, 4, 128, device="cuda")
+    table, lens = torch.arange(4, dtype=torch.int32, device="cuda")[None], ints([60])
+    call = lambda w: tq.paged_decode_attn(p, q, pool, table, lens, window=w)
+    want = call(0)
+    assert not torch.equal(call(5), want)
+    for w in (60, 2**31 - 1, 2**31, 2**32 + 5, 2**40 + 5):
+        assert torch.equal(call(w), want)
+    for w in (-1, -2**32, -2**32 + 5):
+        with pytest.raises(tq.TqError):
+            call(w)
