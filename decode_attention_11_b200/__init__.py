@@ -287,8 +287,8 @@ class Params:
         return p
 
     def as_c(self) -> _Params:
-        p = _Params(self.Pi.data_ptr(), _ptr(self.S), self.k_centroids.data_ptr(), self.k_thresholds.data_ptr(),
-                    self.v_centroids.data_ptr(), self.v_thresholds.data_ptr(), _ptr(self.S_Pi))
+        p = _Params(_ptr(self.Pi), _ptr(self.S), _ptr(self.k_centroids), _ptr(self.k_thresholds),
+                    _ptr(self.v_centroids), _ptr(self.v_thresholds), _ptr(self.S_Pi))
         if self.k_centroids_lo is not None:  # mixed layout
             p.k_centroids_lo, p.k_thresholds_lo = _ptr(self.k_centroids_lo), _ptr(self.k_thresholds_lo)
             p.v_centroids_lo, p.v_thresholds_lo = _ptr(self.v_centroids_lo), _ptr(self.v_thresholds_lo)
@@ -346,8 +346,8 @@ class Cache:
 
     def as_c(self) -> _Cache:
         return _Cache(self.B, self.Hkv, self.T_cap, 128, self.k_bits, self.v_bits, self.qjl_m,
-                      self.k_codes.data_ptr(), _ptr(self.k_signs), self.k_norm.data_ptr(),
-                      _ptr(self.k_rnorm), self.v_codes.data_ptr(), self.v_norm.data_ptr(), self.layout)
+                      _ptr(self.k_codes), _ptr(self.k_signs), _ptr(self.k_norm),
+                      _ptr(self.k_rnorm), _ptr(self.v_codes), _ptr(self.v_norm), self.layout)
 
     def row_bytes(self) -> int:
         nb = 8 if self.layout == TQ_LAYOUT_MIXED else 4
