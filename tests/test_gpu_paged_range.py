@@ -100,3 +100,70 @@ def test_scores_far_below_zero(Hq, big):
     assert np.array_equal(np.isfinite(l), f) and (l[~f] == -np.inf).all()
     # a score's error, with key norms below 29; the product with ln 2 adds two roundings of the value
     assert (np.abs(l[f] - rl[f]) <= 15.0 * big * 29.0 / math.sqrt(128) * SCORE + 2.0**-22 * np.abs(rl[f])).all()
+
+
+# -------------------------------------------------------------------------- fp32 accuracy
+#
+# At ordinary sizes (|q| = 4, key norms 6 .. 20, so scores of one unit or less) the errors are roundings of
+# either sign, which add as a root of squares:
+#   weights   a score of s is off by about s * sqrt(24) * 2^-24 + 2^-22: below 6e-7, and alike for a weight; over
+#             many tokens the output's part of that keeps its size relative to the output, as both fall alike
+#   sums      fp32 over n groups of 16: sqrt(n) 2^-25 of the sum, n <= 148 here: 3.6e-7
+#   rotation  products off by 2^-21.7: 3e-7 of the norm; eight k-steps' sums as much again
+# together below 1.2e-6; 4e-6 allows three times that.  What it has to catch is larger: a sum over tokens that
+# is cut off instead of rounded loses up to 2^-23, on average 2^-24, of the sum so far in each of the 148 groups
+# (8.8e-6 at the end, two thirds of it on the growing sum: 6e-6), and a missing lo part 2^-12 (2.4e-4).
+# lse: one score's error (one token: |q| |k| / sqrt(128) <= 7 times sqrt(24) 2^-24 and 2^-22 = 3.7e-6), and
+# four roundings of a value of at most 14 (3.4e-6): 8e-6.
+OUT_FP32, LSE_FP32 = 4e-6, 8e-6
+
+
+def accurate(out, lse, ref, ref_lse):
+    err = np.linalg.norm(out - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert (err <= OUT_FP32).all(), err.max()
+    assert (np.abs(lse - ref_lse) <= LSE_FP32).all(), np.abs(lse - ref_lse).max()
+
+
+def ordinary_pool(pages, Hkv, ps, kb, vb, seed):
+    pool = filled_pool(pages, Hkv, ps, kb, vb, seed=seed)
+    for n in (pool.k_norm, pool.v_norm):
+        n.mul_(0.5).add_(5.5)  # 6 .. 20
+    pool.k_rnorm.copy_(0.15 * pool.k_norm)
+    return pool
+
+
+def ordinary_queries(B, Hq, seed=9):
+    q = torch.randn(B, Hq, 128, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+    return q * (4.0 / q.norm(dim=-1, keepdim=True))
+
+
+@pytest.mark.parametrize("Hq", [4, 8])
+@pytest.mark.parametrize("kb,vb", [(4, 4), (3, 3), (2, 2)])
+def test_fp32_accuracy(Hq, kb, vb):
+    """One token (the value product and the rotation back alone) to a few thousand."""
+    ps, lens = 32, [1, 1, 2, 15, 100, 1000, 5000]
+    pages = sum(-(-n // ps) for n in lens)
+    pool = ordinary_pool(pages, 1, ps, kb, vb, seed=kb)
+    table = table_for(lens, ps, pages)
+    q = ordinary_queries(len(lens), Hq)
+    out, lse = tq.paged_decode_attn(params(kb, vb), q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    accurate(out.double().cpu().numpy(), lse.double().cpu().numpy(), *reference(q, pool, table, lens))
+
+
+@pytest.mark.parametrize("g", [4, 8])
+def test_fp32_accuracy_of_long_sequences(g):
+    """Four sequences of 128K tokens, 148 groups of 16 and more to a warp; one kv-head of one is compared."""
+    B, Hkv, ps, T, b, kv = 4, 8, 128, 131072, 1, 3
+    pages = B * T // ps
+    pool = ordinary_pool(pages, Hkv, ps, 4, 4, seed=g)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(B, -1).cuda()
+    q = ordinary_queries(B, g * Hkv)
+    out, lse = tq.paged_decode_attn(params(4, 4), q, pool, table, torch.full((B,), T, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    one = tq.Cache.allocate(T // ps, 1, ps, 4, 4)  # that kv-head's pages in order
+    for n in ("k_codes", "k_signs", "k_norm", "k_rnorm", "v_codes", "v_norm"):
+        getattr(one, n)[:, 0] = getattr(pool, n)[table[b].long(), kv]
+    heads = slice(kv * g, kv * g + g)
+    ref, rl = reference(q[b:b + 1, heads], one, torch.arange(T // ps, dtype=torch.int32, device="cuda")[None], [T])
+    accurate(out[b:b + 1, heads].double().cpu().numpy(), lse[b:b + 1, heads].double().cpu().numpy(), ref, rl)
