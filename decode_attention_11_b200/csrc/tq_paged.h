@@ -17,9 +17,8 @@ constexpr int kGroup = kPageTokens;  // tokens of a group: the unit of work, ins
 constexpr float kNoScore = -3.40282347e38f;
 
 // Warps of a split CTA: multiples of four, so that its schedulers are loaded alike.  Up to four heads per
-// unit (nb = 1): 12 warps of 168 registers (128K x 4 in 4 bits: 165 us; 8 or 16 warps 185 us, 13 to 15 190 to
-// 215 us).  Up to eight: 8 warps of 232 (64 sequences to 16K, 3/2 bits: 121 us; 12 warps 127 us, 4 warps
-// 177 us).  These were taken with the sums over tokens in the tensor cores; now they are 171 and 125 us.
+// unit (nb = 1): 12 warps of 168 registers (a call of 4 x 128K tokens in 4 bits: 184 us; 8 warps 194 us, 16 warps
+// 196 us).  Up to eight: 8 warps of 237 (64 sequences to 16K, 3/2 bits: 125 us; 12 warps 134 us, 4 warps 160 us).
 constexpr int paged_warps(int nb) { return nb == 1 ? 12 : 8; }
 
 // Groups of 16 tokens that hold the tokens [first, len) a sequence of length n shows; a length outside

@@ -48,10 +48,14 @@ struct RowArgs {
 };
 
 constexpr int ROWS = 4;
-// Rows per SM up to which the fp64 kernel is used.  It takes 16 us for up to four rows per SM and 10 us for
-// each four more (caches cold, by itself), whatever the rows hold.  The bf16 pipeline takes 32 to 38 us at
-// eight (by widths; up to 47 with rows that its fixups have to do anew), 30 to 38 at twelve against 36; the
-// general kernel that fp32 rows go to takes 46 to 74 us at sixteen against 45, 46 to 76 at twenty against 55.
+// Rows per SM up to which the fp64 kernel is used.  Both sides in us, a call by itself with cold caches (the
+// other routes' range is over 2, 3 and 4 bits):
+//   rows per SM          2      4      8     12     16     20     32
+//   fp64 kernel         15     17     26     35     45     54     82
+//   bf16 pipeline    28-31  28-32  28-35  29-35  30-38  30-38  30-40
+//   fp32 general     29-41  41-58  45-70  46-70  48-74  47-72  49-75
+// (Quantize calls back to back, which overlap in the pipeline and find Pi and S in cache: fp64 kernel 10, 10,
+// 18, 26, 34, 42, 66, pipeline 7 to 18 throughout, general 21 to 64.  A step has other kernels in between.)
 constexpr int kRowsPerSmBf16 = 8, kRowsPerSmF32 = 16;
 constexpr int QT = 256;    // eight warps of 16 matrix rows
 constexpr int XS = D + 2;  // stride of a vector in shared memory (in doubles; no bank conflicts)
@@ -205,12 +209,12 @@ __global__ void __launch_bounds__(QT, 1) quantize_rows(const __grid_constant__ R
 // are four runs of four key codes (slots 32t + 4p ..), eight runs of two value codes (slots
 // 16g + 2p ..) and eight bits of each sign word, so a lane needs a few bytes of each array and writes
 // 16 neighbouring values.  The lanes of a row fetch its codes in 16-byte pieces and pass them through
-// shared memory (each lane its own bytes from global memory: 27 narrow loads, 53 us for 32K tokens in 3/3
-// bits, bound by the L1's tag stage; now 41 us).  Two or three sets of rows per warp, all loads first, took
-// 46 and 53 us.  Bound by the values written and the latency of a row's chain slot -> codes -> values.
+// shared memory (each lane its own bytes from global memory, 27 narrow loads that kept the L1 87% busy, took
+// 53 us for 32K tokens in 3/3 bits where this takes 41 us, calls back to back).  Two or three sets of rows per
+// warp, all loads first, took 46 and 53 us.  Bound by the values written and the latency of a row's chain slot -> codes -> values.
 
 struct ReadArgs {
-  int N, Hkv, pages, ps, qjl;
+  int N, Hkv, pages, ps;
   const int32_t* slots;
   const uint8_t* k_codes;
   const uint8_t* k_signs;
@@ -253,8 +257,8 @@ __device__ __forceinline__ void store16(T* dst, const float (&v)[16]) {
   }
 }
 
-// Threads of a CTA: rows leave in small portions, so that others start (32K tokens, 3/3 bits, 64, 128 and
-// 256 threads: 44, 45 and 48 us with pages in random order).
+// Threads of a CTA: rows leave in small portions, so that others start (a call of 32K tokens, 3/3 bits, slots
+// in random order: 43.2, 43.7 and 45.0 us with 64, 128 and 256 threads).
 constexpr int RT = 64;
 
 template <int KB, int VB, typename T>
@@ -441,7 +445,6 @@ extern "C" tq_status tq_paged_read(const tq_params* params, const tq_cache* pool
   a.Hkv = pool->Hkv;
   a.pages = pool->B;
   a.ps = pool->T_cap;
-  a.qjl = pool->qjl_m ? 1 : 0;
   a.slots = slots;
   a.k_codes = pool->k_codes;
   a.k_signs = pool->k_signs;

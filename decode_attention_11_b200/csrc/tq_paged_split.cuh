@@ -3,18 +3,21 @@
 // Work.  The tokens a sequence shows (all, or a window's) are cut into groups of 16, which never cross
 // a page.  The groups of all units -- a unit is one (sequence, kv-head) and up to eight of its query
 // heads -- are laid end to end and cut into one even, contiguous range per warp, so ragged batches
-// load every warp alike.  The cut follows from the lengths on the device: every CTA sums them itself.
+// load every warp alike.  The cut follows from the lengths on the device: every CTA sums them itself, up to
+// P_LENS sequences; past that it takes the prep kernel's sums.
 // A warp's range is processed as segments, each inside one unit; a segment ends with one
 // (max, sum, o') partial per head, which the merge kernel joins.  A CTA whose whole range lies in one
 // unit (long contexts) joins its warps first, so that a long unit leaves one partial per CTA.
 //
 // Warps run on their own: each keeps a ring of DEPTH groups in shared memory and fetches its next
-// groups itself with 16-byte cp.async (five per lane and group), pages looked up one group ahead.
+// groups itself with 16-byte cp.async (five per lane and group); the page of the next run (the groups of one
+// page) is looked up while the run before it is fetched.
 // (One producer warp with bulk copies per page, an mbarrier ring and CTA-wide segments measured 134 us
 // at 16 sequences x 16K tokens in 4 bits with pages of 64, against 97 us of the same bytes with pages
 // of 128: it was bound by issuing the copies, and short sequences by the barriers at their ends.)
 // Nothing before the first product needs a query, so the rings fill while the prep kernel still runs
-// (programmatic dependent launch).  16 tokens become tensor-core operands:
+// (programmatic dependent launch; past P_LENS sequences only behind it, as its sums are needed first).
+// 16 tokens become tensor-core operands:
 //   scores   D[16 tokens x 8] += A[tokens x dims] B[dims x 8]: A are centroid pairs from a
 //            lane-replicated shared-memory table; a second product with the sign bits placed in fp16
 //            mantissas gives the QJL term

@@ -4,7 +4,8 @@
 // and compact are two launches each: a plan by one CTA (it checks the request, scans the reference
 // counts for free pages, lowest first, and writes its decisions to the workspace), then a grid that
 // carries it out (slots, table rows, page copies), launched as a programmatic dependent of the plan.
-// One CTA is enough for the plan: it reads 4 bytes per page once (64 KB for a pool of 16K pages).
+// One CTA is enough for the plan: it walks the counts twice, 4 bytes per page (to count, then to rank: 64 KB
+// each for a pool of 16K pages), and compact's also writes 4 bytes per page.
 //
 // The copies are bound by memory: the bytes of a page are read and written once, in 16-byte loads,
 // four in flight per thread.

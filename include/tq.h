@@ -384,7 +384,8 @@ tq_status tq_rope(const void* q, int64_t q_stride_n, int64_t q_stride_h, int Hq,
  * calls below, so a serving loop needs no synchronisation and can be captured in a CUDA graph:
  *   table     [n_seq, max_pages]  pool page of each page of a sequence, -1 where it has none
  *   seq_lens  [n_seq]             tokens of each sequence (0: the place is free)
- *   refs      [num_pages]         how many sequences hold the page (0: the page is free)
+ *   refs      [num_pages]         how many sequences hold the page (0: the page is free); 16-byte
+ *                                 aligned
  *   status    [1]                 sticky error bits (below); clear it with a memset
  * Free pages are handed out lowest number first, in the order of the request, so results are
  * reproducible.  Calls on one page table must be ordered on one stream.  Lists of sequences and
@@ -470,6 +471,7 @@ tq_status tq_pages_copy(const tq_cache* caches, int n_caches, const int32_t* src
  *          multiples of 16 bytes
  *   slots  device int32 [N]; a token whose slot is outside [0, num_pages * page_size) is not written
  *          (-1: padding).  Slots must be distinct: a row given twice holds parts of both.
+ *   N      N * Hkv <= 2^30 (0 enqueues nothing)
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED (TQ_LAYOUT_MIXED among them), TQ_ERR_CUDA.
  */
 tq_status tq_paged_quantize(const tq_params* params, const void* k, const void* v, int dtype, int64_t stride_n,
@@ -496,9 +498,11 @@ size_t tq_paged_decode_workspace_size(int B, int Hq, const tq_cache* pool);
 /*
  * Single-token attention of a batch of sequences over a paged pool (the scores and sums of
  * tq_decode_attn).  Lengths and pages are read on the device, so one captured graph serves every step.
- *   q           device [B, Hq, 128] of q_dtype (TQ_F32 or TQ_BF16), contiguous
+ *   q           device [B, Hq, 128] of q_dtype (TQ_F32 or TQ_BF16), contiguous; 1 <= B <= 65536,
+ *               B * Hq <= 2^22
  *   pool        qjl_m 0 or 128, TQ_LAYOUT_PLAIN; Hq % pool->Hkv == 0
- *   table       device int32, row b at table + b * table_stride, max_pages entries each
+ *   table       device int32, row b at table + b * table_stride, max_pages >= 1 entries each, of at
+ *               most 2^30 tokens
  *   seq_lens    device int32 [B]; 0 gives out = 0 and lse = -inf
  *   window      0, or the number of last tokens that are seen (the others' pages are not read)
  *   scale       softmax scale; <= 0 selects 1/sqrt(128)
