@@ -26,6 +26,7 @@ SOURCES = ["tq_host.cpp", "tq_quantize.cu", "tq_quantize_pipe.cu", "tq_decode.cu
            "tq_paged_split_k4.cu"]
 HEADERS = [os.path.join(CSRC, "tq_internal.h"), os.path.join(CSRC, "tq_sm100.h"),
            os.path.join(CSRC, "tq_decode_core.h"), os.path.join(CSRC, "tq_paged.h"),
+           os.path.join(CSRC, "tq_launch.h"),
            os.path.join(CSRC, "tq_paged_split.cuh"),
            os.path.join(INCLUDE, "tq.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",

@@ -16,6 +16,7 @@
 #include <cmath>
 
 #include "tq_decode_core.h"
+#include "tq_launch.h"
 #include "tq_paged.h"
 
 namespace tq {
@@ -506,15 +507,6 @@ __global__ void __launch_bounds__(MT, 2) paged_merge(const __grid_constant__ Mer
 
 // ------------------------------------------------------------------------------------------ host
 
-int attr_of(cudaDeviceAttr attr, int fallback) {
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, attr, dev) != cudaSuccess || v <= 0) {
-    cudaGetLastError();
-    return fallback;
-  }
-  return v;
-}
-
 struct WsPlan {
   int hgroups, nb;
   int64_t units;
@@ -534,23 +526,6 @@ WsPlan ws_plan(int B, int Hq, int Hkv, int ctas) {
   w.err = w.pit + (size_t)MW * 512 * sizeof(uint4);
   w.bytes = w.err + 256;
   return w;
-}
-
-template <typename A>
-tq_status launch_dep(void (*kernel)(const A), int64_t grid, int threads, cudaStream_t s, bool dependent, const char* name,
-                     const A& a) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
-  return TQ_OK;
 }
 
 tq_status check_heads(int B, int Hq, const tq_cache* pool) {
@@ -577,7 +552,7 @@ int paged_reset_errors() {
 extern "C" size_t tq_paged_decode_workspace_size(int B, int Hq, const tq_cache* pool) {
   using namespace tq;
   if (!pool || pool->Hkv < 1 || check_heads(B, Hq, pool) != TQ_OK) return 0;
-  return ws_plan(B, Hq, pool->Hkv, attr_of(cudaDevAttrMultiProcessorCount, 148)).bytes;
+  return ws_plan(B, Hq, pool->Hkv, sm_count()).bytes;
 }
 
 extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q, int q_dtype, int B, int Hq,
@@ -600,7 +575,7 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   if (!q || !out || !workspace || !table || !seq_lens) return fail(TQ_ERR_INVALID_ARG, "q / out / workspace / table / seq_lens is NULL");
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned4(table) || !aligned4(seq_lens) || !aligned4(lse))
     return fail(TQ_ERR_INVALID_ARG, "q / out / workspace must be 16-byte aligned, table / seq_lens / lse 4-byte");
-  const int sms = attr_of(cudaDevAttrMultiProcessorCount, 148);
+  const int sms = sm_count();
   const WsPlan w = ws_plan(B, Hq, pool->Hkv, sms);
   if (workspace_bytes < w.bytes) return fail(TQ_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace_bytes, w.bytes);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
@@ -656,8 +631,8 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   p.before = a.before;
   p.pit = reinterpret_cast<uint4*>(ws + w.pit);
   p.err = a.err;
-  st = launch_dep(qjl ? paged_prep<true> : paged_prep<false>, std::min<int64_t>((w.units * 4 * w.nb + PR - 1) / PR, sms - 1) + 1, MT,
-                  s, false, "paged prep", p);
+  st = launch(qjl ? paged_prep<true> : paged_prep<false>, std::min<int64_t>((w.units * 4 * w.nb + PR - 1) / PR, sms - 1) + 1, MT, 0,
+              s, false, "paged prep", p);
   if (st != TQ_OK) return st;
   st = pool->k_bits == 2   ? paged_split_k2(a, pool->v_bits, qjl, s)
        : pool->k_bits == 3 ? paged_split_k3(a, pool->v_bits, qjl, s)
@@ -683,6 +658,6 @@ extern "C" tq_status tq_paged_decode_attn(const tq_params* params, const void* q
   // 25 us, 384 heads 26 against 25.5, 1024 heads 35 against 26, 9600 heads 147 against 61.  (Sixteen at a
   // time were no faster than eight anywhere, and 4 to 6 us slower up to 1200 heads.)
   const int64_t heads = w.units * m.hgn, room = 2 * sms;
-  if (heads <= room) return launch_dep(paged_merge<true>, heads, MT, s, true, "paged merge", m);
-  return launch_dep(paged_merge<false>, std::min<int64_t>((heads + MW - 1) / MW, room), MT, s, true, "paged merge", m);
+  if (heads <= room) return launch(paged_merge<true>, heads, MT, 0, s, true, "paged merge", m);
+  return launch(paged_merge<false>, std::min<int64_t>((heads + MW - 1) / MW, room), MT, 0, s, true, "paged merge", m);
 }

@@ -42,6 +42,7 @@
 #include <algorithm>
 
 #include "tq_decode_core.h"
+#include "tq_launch.h"
 #include "tq_paged.h"
 
 namespace tq {
@@ -141,6 +142,7 @@ __device__ __forceinline__ uint2 lut64(uint32_t p) {
   asm("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(p));
   return v;
 }
+// mma16816 without `volatile`, so that the compiler may interleave the products with the lookups.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -706,21 +708,10 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
 
 template <int KB, int VB, bool QJL, int NB>
 tq_status launch_paged(const PagedArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(paged_split<KB, VB, QJL, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(paged_split<KB, VB, QJL, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM);
   if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "smem attribute: %s", cudaGetErrorString(e));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.ctas);
-  cfg.blockDim = dim3((PLayout<KB, VB, QJL, NB>::THREADS));
-  cfg.dynamicSmemBytes = P_SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // dependent of the prep kernel
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_split<KB, VB, QJL, NB>, a);
-  if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "paged split launch: %s", cudaGetErrorString(e));
-  return TQ_OK;
+  // (a dependent of the prep kernel)
+  return launch(paged_split<KB, VB, QJL, NB>, a.ctas, PLayout<KB, VB, QJL, NB>::THREADS, P_SMEM, stream, true, "paged split", a);
 }
 
 template <int KB, int VB>

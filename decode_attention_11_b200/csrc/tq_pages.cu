@@ -15,6 +15,7 @@
 #include <climits>
 
 #include "tq_internal.h"
+#include "tq_launch.h"
 
 namespace tq {
 namespace {
@@ -546,30 +547,12 @@ CopyArgs copy_args(const tq_cache* c, int n) {
 }
 
 // CTAs of a launch with `items` units of work, at most all that can be resident.
-int grid_for(int64_t items) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    sms = 148;
-  }
-  return (int)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sms * CTAS_PER_SM));
-}
+int grid_for(int64_t items) { return (int)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)sm_count() * CTAS_PER_SM)); }
 
-// Launch `kernel` as a programmatic dependent of the stream's last kernel (the plan).
+// A kernel that carries out the plan before it.
 template <typename... K, typename... A>
-tq_status launch_after(void (*kernel)(K...), int grid, cudaStream_t s, const char* name, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(COPY_THREADS);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s launch: %s", name, cudaGetErrorString(e));
-  return TQ_OK;
+tq_status launch_after(void (*kernel)(K...), int grid, cudaStream_t s, const char* name, const A&... args) {
+  return launch(kernel, grid, COPY_THREADS, 0, s, true, name, args...);
 }
 
 tq_status launched(const char* name) {
