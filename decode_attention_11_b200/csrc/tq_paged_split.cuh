@@ -564,8 +564,8 @@ __global__ void __launch_bounds__(PLayout<KB, VB, QJL, NB>::THREADS, 1) paged_sp
           const float e0 = ex2(sc0[x] - m_run[x]);  // ex2(-inf) = 0 for rows that are not shown
           const float e1 = ex2(sc1[x] - m_run[x]);
           l_run[x] += e0 + e1;
-          p0[x] = e0 * (nv0 * vscale[x]);
-          p1[x] = e1 * (nv1 * vscale[x]);
+          p0[x] = e0 * nv0 * vscale[x];  // (in this order: norm times scale can pass fp32 where exp is 0)
+          p1[x] = e1 * nv1 * vscale[x];
         }
         if constexpr (NB == 1) {
           bp[0][0] = movmatrix_trans(hilo_half2(p0[0]));

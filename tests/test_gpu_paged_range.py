@@ -167,3 +167,31 @@ def test_fp32_accuracy_of_long_sequences(g):
     heads = slice(kv * g, kv * g + g)
     ref, rl = reference(q[b:b + 1, heads], one, torch.arange(T // ps, dtype=torch.int32, device="cuda")[None], [T])
     accurate(out[b:b + 1, heads].double().cpu().numpy(), lse[b:b + 1, heads].double().cpu().numpy(), ref, rl)
+
+
+@pytest.mark.parametrize("Hq", [4, 8])
+def test_value_norms_over_the_whole_range(Hq):
+    """Norms of 1e-8 and of 1e30 in one sequence, the large ones at scores 200 below the maximum (e^-200 1e38
+    is below 1e-48 of the output); next to the token that has the weight and in other groups."""
+    away = [1, -1, 5, 16, -16, 40]
+    B, ps, T = len(away), 16, 500
+    lens = [T] * B
+    pages = B * (-(-T // ps))
+    pool = filled_pool(pages, 1, ps, 4, 4, seed=4)
+    pool.k_norm.mul_(0.1)
+    pool.k_rnorm.mul_(0.1)
+    pool.v_norm.mul_(1e-9)
+    table = table_for(lens, ps, pages)
+    q = like_queries(B, Hq)
+    norms = []
+    for b, d in enumerate(away):
+        i, n = raise_score(pool, table, q, b, 240 + b, 272 + b, 200.0)
+        norms.append(n)
+        pool.v_norm[table[b, (i + d) // ps].long(), 0, (i + d) % ps] = 1e30
+    out, lse = tq.paged_decode_attn(params(4, 4), q, pool, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    return_lse=True)
+    ref, rl = reference(q, pool, table, lens)
+    err = np.linalg.norm(out.double().cpu().numpy() - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert (err <= ALL_WEIGHT).all(), err
+    tol = 15.0 * np.array(norms)[:, None] / math.sqrt(128) * SCORE + 2.0**-22 * np.abs(rl)
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= tol).all()
