@@ -1599,7 +1599,7 @@ int decode_reset_errors() {
 
 extern "C" int tq_decode_device_errors(void) {
   unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, tq::g_decode_error, sizeof(v)) != cudaSuccess) return -1;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&v, tq::g_decode_error, sizeof(v)) != cudaSuccess) return -1;
   bool ok = false;
   const unsigned int paged = tq::paged_decode_errors(&ok);
   return ok ? (int)(v | paged) : -1;

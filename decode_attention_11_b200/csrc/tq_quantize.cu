@@ -1112,9 +1112,11 @@ extern "C" tq_status tq_quantize(const tq_params* params, const void* k, const v
                          : launch<__nv_bfloat16>(cache->k_bits, cache->v_bits, a, sms, s);
 }
 
+// (The copies of these diagnostics wait for the default stream alone: streams that do not block on it, like
+// those of PyTorch, are waited for by the synchronization before them.)
 extern "C" int tq_quantize_device_errors(void) {
   unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, tq::g_quantize_error, sizeof(v)) != cudaSuccess) return -1;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&v, tq::g_quantize_error, sizeof(v)) != cudaSuccess) return -1;
   const unsigned int p = tq::pipe_device_errors();
   if (p == 0xffffffffu) return -1;
   return (int)(v | p);
@@ -1122,28 +1124,28 @@ extern "C" int tq_quantize_device_errors(void) {
 
 extern "C" long long tq_quantize_vector_fixups(void) {
   unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, tq::g_quantize_vector_fixups, sizeof(v)) != cudaSuccess) return -1;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&v, tq::g_quantize_vector_fixups, sizeof(v)) != cudaSuccess) return -1;
   const long long p = tq::pipe_vector_fixups();
   return p < 0 ? -1 : (long long)v + p;
 }
 
 extern "C" long long tq_quantize_code_fixups(void) {
   unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, tq::g_quantize_code_fixups, sizeof(v)) != cudaSuccess) return -1;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&v, tq::g_quantize_code_fixups, sizeof(v)) != cudaSuccess) return -1;
   const long long p = tq::pipe_code_fixups();
   return p < 0 ? -1 : (long long)v + p;
 }
 
 extern "C" long long tq_quantize_exempt_codes(void) {
   unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, tq::g_quantize_exempt_codes, sizeof(v)) != cudaSuccess) return -1;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&v, tq::g_quantize_exempt_codes, sizeof(v)) != cudaSuccess) return -1;
   const long long p = tq::pipe_exempt_codes();
   return p < 0 ? -1 : (long long)v + p;
 }
 
 extern "C" long long tq_quantize_exempt_signs(void) {
   unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, tq::g_quantize_exempt_signs, sizeof(v)) != cudaSuccess) return -1;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(&v, tq::g_quantize_exempt_signs, sizeof(v)) != cudaSuccess) return -1;
   const long long p = tq::pipe_exempt_signs();
   return p < 0 ? -1 : (long long)v + p;
 }
@@ -1157,7 +1159,7 @@ extern "C" tq_status tq_debug_quantize_stall(int enable, long long wait_cycles) 
 
 extern "C" int tq_reset_device_errors(void) {
   const unsigned int z = 0;
-  if (cudaMemcpyToSymbol(tq::g_quantize_error, &z, sizeof(z)) != cudaSuccess) return -1;
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyToSymbol(tq::g_quantize_error, &z, sizeof(z)) != cudaSuccess) return -1;
   if (tq::pipe_reset_errors() != 0) return -1;
   return tq::decode_reset_errors();
 }

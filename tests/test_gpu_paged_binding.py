@@ -156,3 +156,31 @@ def test_window_past_32_bits_sees_all():
     for w in (-1, -2**32, -2**32 + 5):
         with pytest.raises(tq.TqError):
             call(w)
+
+
+# -------------------------------------------------------------------------- diagnostics
+
+def test_diagnostics_see_calls_on_every_stream():
+    """Error bits and counters are read after what any stream still has to do."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pool = tq.Cache.allocate(40, 4, 64, 4, 4, 0)
+    p = tq.Params.create(torch.eye(128).numpy(), None, 4, 4)
+    q = torch.randn(1, 4, 128, device="cuda")
+    bad, lens = torch.full((1, 4), 10**6, dtype=torch.int32, device="cuda"), ints([60])
+    x = torch.randn(2500, 4, 128, generator=g, device="cuda").to(torch.bfloat16)
+    slots = torch.arange(2500, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    tq.reset_device_errors()
+    for _ in range(2):
+        count = tq.quantize_code_fixups()
+        keep_busy(side)
+        tq.paged_quantize(p, x, x, pool, slots, stream=side)
+        assert tq.quantize_code_fixups() > count
+        keep_busy(side)
+        tq.paged_decode_attn(p, q, pool, bad, lens, stream=side)
+        assert tq.decode_device_errors() == 16
+        keep_busy(side)
+        tq.paged_decode_attn(p, q, pool, bad, lens, stream=side)
+        tq.reset_device_errors()
+        torch.cuda.synchronize()
+        assert tq.decode_device_errors() == 0
