@@ -417,6 +417,7 @@ size_t tq_pages_workspace_size(const tq_page_table* pt, int n);
  *   seqs, new_tokens  device int32 [n], the sequences distinct
  *   slots             device int32 [n_slots] out (NULL when n_slots = 0): the slots of the new tokens,
  *                     sequence after sequence in the order of the list, then -1 up to n_slots
+ *                     (with n_slots = 0 none are written, and there is no room to check)
  * On an error (NO_ROOM, BAD_INDEX, BAD_LENGTH, SHARED) every slot is -1 and nothing else changes.
  * Errors: TQ_ERR_INVALID_ARG, TQ_ERR_WORKSPACE, TQ_ERR_CUDA.
  */

@@ -184,3 +184,27 @@ def test_diagnostics_see_calls_on_every_stream():
         tq.reset_device_errors()
         torch.cuda.synchronize()
         assert tq.decode_device_errors() == 0
+
+
+def test_rope_gradient_in_a_graph():
+    """Forward and backward captured together: a replay turns the inputs, positions and gradients as they are then."""
+    torch.manual_seed(1)
+    q = torch.randn(33, 4, 128, device="cuda", requires_grad=True)
+    g = torch.randn(33, 4, 128, device="cuda")
+    pos = torch.arange(33, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out, _ = tq.rope(q, None, pos)
+        grad, = torch.autograd.grad(out, q, g)
+    for _ in range(2):
+        with torch.no_grad():
+            q.copy_(torch.randn_like(q))
+        g.copy_(torch.randn_like(g))
+        pos.add_(1000)
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.no_grad():
+            assert torch.equal(out, tq.rope(q, None, pos)[0])
+            assert torch.equal(grad, tq.rope(g, None, pos, inverse=True)[0])
